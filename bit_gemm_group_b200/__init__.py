@@ -42,6 +42,7 @@ EXPORTED = (
     "wq_channel_absmax", "wq_smooth_scales", "wq_quantize_i8_smooth", "wq_quant_act_i8_smooth",
     "wq_gemm_w8a8_smooth", "wq_quant_kv", "wq_quantize_fp8_rows", "wq_gemm_fp8",
     "wq_gptq_workspace_bytes", "wq_gptq_quantize", "wq_gemm_w8a16",
+    "wq_quantize_fp8_block", "wq_fp8_block_workspace_bytes", "wq_gemm_fp8_block",
 )
 
 
@@ -114,6 +115,12 @@ def _declare(L):
     L.wq_gptq_workspace_bytes.argtypes = [_I64, _I64]
     L.wq_gptq_workspace_bytes.restype = _SZ
     L.wq_gptq_quantize.argtypes = [_P, _INT, _I64, _I64, _P, _INT, _INT, _P, _P, _P, _P, _SZ, _P]
+    L.wq_quantize_fp8_block.argtypes = [_P, _INT, _I64, _I64, _INT, _P, _P, _P]
+    L.wq_fp8_block_workspace_bytes.argtypes = [_I64, _I64, _I64]
+    L.wq_fp8_block_workspace_bytes.restype = _SZ
+    L.wq_gemm_fp8_block.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _SZ, _P]
+    for name in ("wq_quantize_fp8_block", "wq_gemm_fp8_block"):
+        getattr(L, name).restype = _INT
     for name in ("wq_quantize_pack", "wq_dequant", "wq_gemm_w4a16", "wq_quant_act_i8",
                  "wq_gemm_w8a8", "wq_get_device_status", "wq_channel_absmax",
                  "wq_smooth_scales", "wq_quantize_i8_smooth", "wq_quant_act_i8_smooth",
@@ -366,6 +373,63 @@ def wq_gemm_w8a16(X, Wq, w_fmt, w_scales, Y, stream=None):
     _check(st, "wq_gemm_w8a16")
 
 
+def _same_device(*tensors):
+    """The device that all of the tensors are on; a call's pointers belong to one."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected a torch.Tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise WQError(WQ_ERR_ARG, f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _typed(t, dtype, what):
+    if isinstance(t, torch.Tensor) and t.dtype != dtype:
+        raise WQError(WQ_ERR_ARG, f"{what} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _on(dev):
+    """Make `dev` current for a call: the library works on the current device."""
+    if dev.type != "cuda":
+        raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
+    return torch.cuda.device(dev)
+
+
+def wq_quantize_fp8_block(A, block_rows, q, scales, stream=None):
+    R, K = A.shape
+    KB = -(-K // 128)
+    _fits(q, R * K, "q")
+    _fits(_typed(scales, torch.float32, "scales"),
+          4 * KB * (-(-R // block_rows) if block_rows > 0 else 0), "scales")
+    with _on(_same_device(A, q, scales)):
+        st = lib().wq_quantize_fp8_block(_ptr(A), _DTYPE_TAG.get(A.dtype, -1), R, K, block_rows,
+                                         _ptr(q), _ptr(scales), _stream(stream))
+    _check(st, "wq_quantize_fp8_block")
+
+
+def wq_fp8_block_workspace_bytes(M, N, K):
+    return int(lib().wq_fp8_block_workspace_bytes(M, N, K))
+
+
+def wq_gemm_fp8_block(X, Wq, w_scales, Y, ws, stream=None):
+    M, K = X.shape
+    N, KB = Wq.shape[0], -(-K // 128)
+    _fits(Wq, N * K, "Wq")
+    _fits(_typed(w_scales, torch.float32, "w_scales"), 4 * -(-N // 128) * KB, "w_scales")
+    _fits(Y, 2 * M * N, "Y")
+    with _on(_same_device(X, Wq, w_scales, Y, ws)):
+        st = lib().wq_gemm_fp8_block(_bf16(X, "X"), M, K, _ptr(Wq), _ptr(w_scales), N,
+                                     _bf16(Y, "Y"), _ptr(ws), ws.numel() * ws.element_size(),
+                                     _stream(stream))
+    _check(st, "wq_gemm_fp8_block")
+
+
 def wq_gptq_quantize(W, U, group_size, sym, codes, scales, zeros, ws, stream=None):
     N, K = W.shape
     G = _groups(K, group_size)
@@ -533,6 +597,31 @@ def gemm_fp8(X, Wq, w_scales, want_acc=False):
     acc = torch.empty((M, N), dtype=torch.float32, device=X.device) if want_acc else None
     wq_gemm_fp8(X, Wq, w_scales, Y, ws, acc)
     return (Y, acc) if want_acc else Y
+
+
+def quantize_fp8_block(A, block_rows=128):
+    """E4M3 codes uint8 [R, K] and fp32 scales [ceil(R / block_rows), ceil(K / 128)]:
+    block_rows 128 for a weight, 1 for activations."""
+    R, K = A.shape
+    q = torch.empty((R, K), dtype=torch.uint8, device=A.device)
+    s = torch.empty((-(-R // block_rows), -(-K // 128)), dtype=torch.float32, device=A.device)
+    wq_quantize_fp8_block(A, block_rows, q, s)
+    return q, s
+
+
+def gemm_fp8_block(X, Wq, w_scales, ws=None):
+    """Y = X W^T with X bf16 [M, K] quantized per token and 128 input dims and W
+    [N, K] from quantize_fp8_block(W, 128).  ws: a uint8 workspace of
+    wq_fp8_block_workspace_bytes(M, N, K) bytes to reuse from call to call."""
+    M, K = X.shape
+    N = Wq.shape[0]
+    Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+    if ws is None:
+        with _on(X.device):
+            n = wq_fp8_block_workspace_bytes(M, N, K)
+        ws = torch.empty((max(1, n),), dtype=torch.uint8, device=X.device)
+    wq_gemm_fp8_block(X, Wq, w_scales, Y, ws)
+    return Y
 
 
 # ------------------------------------------------------------------ GPTQ helper

@@ -77,4 +77,13 @@ int launch_gemm_w8a8(const void* X, int64_t M, int64_t K, const void* Wq, const 
                      const float* smooth, int64_t N, void* Y, void* ws, void* acc_out,
                      cudaStream_t s);
 
+// Block-scaled FP8: scales are [ceil(R / rows), KB] with KB = ceil(K / 128), or
+// (rows == 1, transposed) [KB, ld]; `counters` (nullable) are set to zero.
+int launch_quantize_fp8_block(const void* X, int dtype, int64_t R, int64_t K, int rows, void* q,
+                              float* scales, int64_t ld, bool transposed, int* counters,
+                              int n_counters, cudaStream_t s);
+size_t fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int launch_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, const float* sw,
+                          int64_t N, void* Y, void* ws, cudaStream_t s);
+
 }  // namespace wq_host

@@ -369,6 +369,52 @@ int wq_gemm_w8a16(const void* X, int64_t M, int64_t K, const void* Wq, int w_fmt
                                     Y, as_stream(stream));
 }
 
+// ------------------------------------------------------- block-scaled FP8
+
+int wq_quantize_fp8_block(const void* A, int a_dtype, int64_t R, int64_t K, int block_rows,
+                          void* q, void* scales, void* stream) {
+  if (R < 0 || K < 0) return WQ_ERR_ARG;
+  if (a_dtype != WQ_F32 && a_dtype != WQ_BF16 && a_dtype != WQ_F16) return WQ_ERR_ARG;
+  if (block_rows != 1 && block_rows != 128) return WQ_ERR_UNSUPPORTED;
+  if ((K % 16) != 0) return WQ_ERR_ALIGN;
+  if (R > (int64_t(1) << 31) || K > (int64_t(1) << 24)) return WQ_ERR_UNSUPPORTED;
+  if (R == 0 || K == 0) return WQ_OK;
+  if (!A || !q || !scales) return WQ_ERR_ARG;
+  if (!aligned16(A) || !aligned16(q) || !aligned16(scales)) return WQ_ERR_ALIGN;
+  int st = wq_host::ensure_device();
+  if (st != WQ_OK) return st;
+  return wq_host::launch_quantize_fp8_block(A, a_dtype, R, K, block_rows, q,
+                                            static_cast<float*>(scales), (K + 127) / 128, false,
+                                            nullptr, 0, as_stream(stream));
+}
+
+size_t wq_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 24)) return 0;
+  wq_host::ensure_device();  // the size depends on the device's SM count
+  return wq_host::fp8_block_workspace_bytes(M, N, K);
+}
+
+int wq_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, const void* w_scales,
+                      int64_t N, void* Y, void* ws, size_t ws_bytes, void* stream) {
+  if (M < 0 || K < 0 || N < 0) return WQ_ERR_ARG;
+  if ((K % 16) != 0 || (N % 8) != 0) return WQ_ERR_ALIGN;
+  if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 24))
+    return WQ_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return WQ_OK;
+  if (K == 0) return WQ_ERR_ARG;
+  if (!X || !Wq || !w_scales || !Y) return WQ_ERR_ARG;
+  if (!aligned16(X) || !aligned16(Wq) || !aligned16(w_scales) || !aligned16(Y) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return WQ_ERR_ALIGN;
+  if (!ws) return WQ_ERR_WORKSPACE;
+  int st = wq_host::ensure_device();
+  if (st != WQ_OK) return st;
+  if (ws_bytes < wq_host::fp8_block_workspace_bytes(M, N, K)) return WQ_ERR_WORKSPACE;
+  return wq_host::launch_gemm_fp8_block(X, M, K, Wq, static_cast<const float*>(w_scales), N, Y,
+                                        ws, as_stream(stream));
+}
+
 // -------------------------------------------------------------------- GPTQ
 
 size_t wq_gptq_workspace_bytes(int64_t N, int64_t K) {

@@ -332,6 +332,43 @@ WQ_API int wq_gemm_fp8(const void *X, int64_t M, int64_t K, const void *Wq,
                        size_t ws_bytes, void *acc_out, void *stream);
 
 /*
+ * Block-scaled FP8 E4M3 W8A8: the recipe of wq_gemm_fp8 with one scale for each
+ * block of 128 input dims instead of one per row, per token for activations and
+ * shared by 128 output channels for weights (the per-group granularity of [P4]
+ * sec. 2.2 applied to both operands), so an outlier coarsens only its block.
+ *
+ * wq_quantize_fp8_block -- E4M3 codes q [R, K] of A [R, K] (a_dtype WQ_F32 /
+ * WQ_BF16 / WQ_F16) and fp32 scales [ceil(R / block_rows), ceil(K / 128)]:
+ * s = max(max |x| over the block / 448, 1e-8), q = E4M3(x / s) (IEEE fp32
+ * divisions, round to nearest even, saturating).  block_rows is 128 (weights)
+ * or 1 (activations), others are WQ_ERR_UNSUPPORTED.  Blocks at the lower and
+ * right edge may be partial.  Requires K % 16 == 0.  A non-finite element is
+ * reported as WQ_ERR_NONFINITE in the device status; its block's codes are
+ * then unspecified.
+ */
+WQ_API int wq_quantize_fp8_block(const void *A, int a_dtype, int64_t R, int64_t K,
+                                 int block_rows, void *q, void *scales, void *stream);
+
+/*
+ * wq_gemm_fp8_block -- Y[m, n] = bf16(sum_J sx[m, J] * w_scales[n / 128, J] *
+ * acc_J[m, n]) with acc_J = sum over the 128 input dims of block J of
+ * E4M3(qx[m, k]) * E4M3(Wq[n, k]) on the tensor cores (tcgen05.mma
+ * kind::f8f6f4); the sum over J is held in fp32.  X bf16 [M, K] is quantized
+ * into ws first (as wq_quantize_fp8_block with block_rows 1); Wq [N, K] and
+ * w_scales [ceil(N / 128), ceil(K / 128)] come from wq_quantize_fp8_block with
+ * block_rows 128.  M from 1: few tokens run a kernel that streams every weight
+ * byte once with the work split evenly over the SMs.  Results do not depend
+ * on timing (partial sums are joined in a fixed order).  Requires K % 16 == 0
+ * and N % 8 == 0.  ws: wq_fp8_block_workspace_bytes(M, N, K) bytes on the
+ * current device, 256-byte aligned, any contents; calls that may overlap on
+ * the GPU need separate workspaces.
+ */
+WQ_API size_t wq_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);
+WQ_API int wq_gemm_fp8_block(const void *X, int64_t M, int64_t K, const void *Wq,
+                             const void *w_scales, int64_t N, void *Y, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/*
  * wq_gptq_quantize -- GPTQ INT4 group-wise quantization with error feedback
  * ([P4] sec. 4.3).  Columns (input dims) are quantized in order; each column's
  * error (w - w_hat) / U[i, i] is pushed into the columns not yet quantized
