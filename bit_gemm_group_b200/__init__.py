@@ -43,6 +43,7 @@ EXPORTED = (
     "wq_gemm_w8a8_smooth", "wq_quant_kv", "wq_quantize_fp8_rows", "wq_gemm_fp8",
     "wq_gptq_workspace_bytes", "wq_gptq_quantize", "wq_gemm_w8a16",
     "wq_quantize_fp8_block", "wq_fp8_block_workspace_bytes", "wq_gemm_fp8_block",
+    "wq_kv8_append", "wq_attn_kv8_workspace_bytes", "wq_attn_kv8",
 )
 
 
@@ -119,7 +120,13 @@ def _declare(L):
     L.wq_fp8_block_workspace_bytes.argtypes = [_I64, _I64, _I64]
     L.wq_fp8_block_workspace_bytes.restype = _SZ
     L.wq_gemm_fp8_block.argtypes = [_P, _I64, _I64, _P, _P, _I64, _P, _P, _SZ, _P]
-    for name in ("wq_quantize_fp8_block", "wq_gemm_fp8_block"):
+    kv8 = [_I64, _I64, _INT, _P, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P,
+           _I64, _I64, _INT]
+    L.wq_kv8_append.argtypes = [_P, _P, _INT, _I64, _I64, _I64] + kv8 + [_P]
+    L.wq_attn_kv8_workspace_bytes.argtypes = [_I64] * 5
+    L.wq_attn_kv8_workspace_bytes.restype = _SZ
+    L.wq_attn_kv8.argtypes = [_P, _INT, _I64, _I64, _I64] + kv8 + [ctypes.c_float, _P, _P, _SZ, _P]
+    for name in ("wq_quantize_fp8_block", "wq_gemm_fp8_block", "wq_kv8_append", "wq_attn_kv8"):
         getattr(L, name).restype = _INT
     for name in ("wq_quantize_pack", "wq_dequant", "wq_gemm_w4a16", "wq_quant_act_i8",
                  "wq_gemm_w8a8", "wq_get_device_status", "wq_channel_absmax",
@@ -430,6 +437,87 @@ def wq_gemm_fp8_block(X, Wq, w_scales, Y, ws, stream=None):
     _check(st, "wq_gemm_fp8_block")
 
 
+def _rows_ptr(t, what):
+    """(pointer, elements between rows) of a [n, heads, D] tensor whose rows may be
+    columns of a wider one (a slice of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not t.is_cuda:
+        raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
+    n, heads, D = t.shape
+    ld = t.stride(0) if n > 1 else heads * D
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+        raise WQError(WQ_ERR_ARG, f"{what}: the heads of a row must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _kv8_args(cache, heads, D, block_table, cu_rows, seq_lens, max_new, rope):
+    """The arguments that the append and the attention share, checked against the
+    tensors' extents; heads and D are those of the call's rows."""
+    kq, ks, vq, vs = cache
+    if kq.dim() != 4 or kq.shape != vq.shape or kq.dtype != vq.dtype:
+        raise WQError(WQ_ERR_ARG, "cache: kq and vq must be [pages, heads, page_size, D], alike")
+    if kq.dtype not in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+        raise WQError(WQ_ERR_ARG, f"cache: codes must be int8, or uint8 for E4M3, got {kq.dtype}")
+    P, kv, T, cd = kq.shape
+    if cd != D:
+        raise WQError(WQ_ERR_ARG, f"cache holds heads of {cd} elements, the rows of {D}")
+    for t, what in ((ks, "ks"), (vs, "vs")):
+        _fits(_typed(t, torch.float32, what), 4 * P * kv, what)
+    for t, what in ((block_table, "block_table"), (cu_rows, "cu_rows"), (seq_lens, "seq_lens")):
+        _typed(t, torch.int32, what)
+    B, width = block_table.shape
+    _fits(cu_rows, 4 * (B + 1), "cu_rows")
+    _fits(seq_lens, 4 * B, "seq_lens")
+    cos, sin, inter = (None, None, False) if rope is None else rope
+    rot, max_pos = 0, 0
+    if cos is not None:
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if sin is None or sin.shape != cos.shape:
+            raise WQError(WQ_ERR_ARG, "cos and sin must have the same shape")
+        _typed(cos, torch.float32, "cos")
+        _typed(sin, torch.float32, "sin")
+    fmt = WQ_W8_INT8 if kq.dtype == torch.int8 else WQ_W8_E4M3
+    return [kv, D, fmt, _ptr(kq), _ptr(ks), _ptr(vq), _ptr(vs), P, T, _ptr(block_table), width,
+            _ptr(cu_rows), _ptr(seq_lens), B, int(max_new), _ptr(cos), _ptr(sin), rot, max_pos,
+            int(bool(inter))]
+
+
+def wq_kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope=None, stream=None):
+    n, heads, D = K.shape
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise WQError(WQ_ERR_ARG, "K and V must have the same shape and dtype")
+    if cache[0].dim() == 4 and cache[0].shape[1] != heads:
+        raise WQError(WQ_ERR_ARG, f"cache has {cache[0].shape[1]} heads, K has {heads}")
+    cos, sin = (None, None) if rope is None else rope[:2]
+    with _on(_same_device(K, V, *cache, block_table, cu_rows, seq_lens, cos, sin)):
+        (kp, ldk), (vp, ldv) = _rows_ptr(K, "K"), _rows_ptr(V, "V")
+        st = lib().wq_kv8_append(kp, vp, _DTYPE_TAG.get(K.dtype, -1), n, ldk, ldv,
+                                 *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens,
+                                            max_new, rope), _stream(stream))
+    _check(st, "wq_kv8_append")
+
+
+def wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new):
+    return int(lib().wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new))
+
+
+def wq_attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new, scale, out, ws, rope=None,
+                stream=None):
+    n, heads, D = Q.shape
+    if out.dtype != Q.dtype:
+        raise WQError(WQ_ERR_ARG, f"out must be {Q.dtype}, got {out.dtype}")
+    _fits(out, Q.numel() * Q.element_size(), "out")
+    cos, sin = (None, None) if rope is None else rope[:2]
+    with _on(_same_device(Q, *cache, block_table, cu_rows, seq_lens, out, ws, cos, sin)):
+        qp, ldq = _rows_ptr(Q, "Q")
+        st = lib().wq_attn_kv8(qp, _DTYPE_TAG.get(Q.dtype, -1), n, ldq, heads,
+                               *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens,
+                                          max_new, rope), float(scale), _ptr(out), _ptr(ws),
+                               ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "wq_attn_kv8")
+
+
 def wq_gptq_quantize(W, U, group_size, sym, codes, scales, zeros, ws, stream=None):
     N, K = W.shape
     G = _groups(K, group_size)
@@ -622,6 +710,47 @@ def gemm_fp8_block(X, Wq, w_scales, ws=None):
         ws = torch.empty((max(1, n),), dtype=torch.uint8, device=X.device)
     wq_gemm_fp8_block(X, Wq, w_scales, Y, ws)
     return Y
+
+
+# ------------------------------------------------- paged 8-bit KV cache helpers
+
+def kv8_cache(pages, kv_heads, page_size, D, dtype=torch.int8, device="cuda"):
+    """An empty paged cache (kq, ks, vq, vs): codes [pages, kv_heads, page_size, D] of
+    dtype int8, or uint8 for E4M3, and fp32 scales [pages, kv_heads]."""
+    codes = [torch.zeros((pages, kv_heads, page_size, D), dtype=dtype, device=device)
+             for _ in range(2)]
+    scales = [torch.zeros((pages, kv_heads), dtype=torch.float32, device=device)
+              for _ in range(2)]
+    return codes[0], scales[0], codes[1], scales[1]
+
+
+def kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope=None):
+    """Write the rows K, V [n, kv_heads, D] at the end of their sequences, K rotated.
+
+    cu_rows int32 [B + 1] and seq_lens int32 [B] (with the new rows) say whose rows they
+    are; max_new bounds a sequence's rows; rope is (cos, sin, interleaved) with fp32
+    tables [max_pos, rot_dim / 2], or None."""
+    wq_kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope)
+
+
+def attn_kv8_workspace(B, heads, kv_heads, D, max_new, device):
+    """A workspace for attn_kv8, to be reused from call to call on one stream."""
+    with _on(torch.empty(0, device=device).device):
+        n = wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new)
+    return torch.empty((max(1, n),), dtype=torch.uint8, device=device)
+
+
+def attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new, scale=None, rope=None, ws=None):
+    """Causal attention of Q [n, heads, D] over the paged cache (after the rows' append,
+    with the same cu_rows and seq_lens): [n, heads, D].  scale: 1 / sqrt(D) by default."""
+    n, heads, D = Q.shape
+    out = torch.empty((n, heads, D), dtype=Q.dtype, device=Q.device)
+    if ws is None:
+        ws = attn_kv8_workspace(block_table.shape[0], heads, cache[0].shape[1], D, max_new,
+                                Q.device)
+    wq_attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new,
+                D ** -0.5 if scale is None else scale, out, ws, rope)
+    return out
 
 
 # ------------------------------------------------------------------ GPTQ helper

@@ -86,4 +86,23 @@ size_t fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int launch_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, const float* sw,
                           int64_t N, void* Y, void* ws, cudaStream_t s);
 
+// Paged 8-bit KV cache: what its append and its attention share.
+struct Kv8 {
+  void *kq, *vq;
+  float *ks, *vs;
+  int fmt;  // WQ_W8_INT8 or WQ_W8_E4M3
+  int64_t pages, kv_heads, page, D;
+  const int *table, *cu, *lens;
+  int64_t B, width, rows, max_new;
+  const float *cos, *sin;
+  int64_t rot;
+  bool interleaved;
+};
+int launch_kv8_append(const void* K, const void* V, int dtype, int64_t ldk, int64_t ldv,
+                      const Kv8& a, int max_pos, cudaStream_t s);
+size_t attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                int64_t max_q);
+int launch_attn_kv8(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
+                    int max_pos, float scale, void* out, void* ws, cudaStream_t s);
+
 }  // namespace wq_host

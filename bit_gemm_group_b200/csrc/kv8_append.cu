@@ -1,0 +1,175 @@
+// kv8_append.cu -- write new key and value rows into the paged 8-bit cache,
+// keys rotated by their position on the way.
+//
+// For each (page, head) that receives rows, keys and values apart:
+//   s' = max(max |x| of the new rows / qmax, 1e-8), and at least the block's
+//        scale s where the page already holds older rows of the sequence
+//   older codes c -> round(c s / s') where s' > s;  new codes round(x / s')
+// qmax = 127 (int8) or 448 (E4M3).
+//
+// Bound by HBM: 2 (4) bytes read and 1 written per element.  One CTA per
+// (sequence, touched page, head, keys or values) holds the page's new rows in
+// registers between the maximum and the codes, so a block is read once and its
+// scale is written by one CTA, with no atomics.  In a decode step a CTA has one
+// row; older codes are read only when the new row raises the maximum.
+#include "kv8.cuh"
+
+namespace wq {
+namespace kv8 {
+
+constexpr int STEPS = 8;  // 8-element pieces per thread; T D / 64 threads
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(512)
+    kv8_append_kernel(const T* __restrict__ K, const T* __restrict__ V, int64_t ldk, int64_t ldv,
+                      int D, Cache c, Batch bt, Rope rp, int slots, int* status) {
+  constexpr float TOP = FMT == WQ_W8_INT8 ? 127.f : 448.f;
+  __shared__ float red[16];
+  int64_t id = blockIdx.x;
+  const bool is_v = id & 1;
+  id >>= 1;
+  const int h = int(id % c.heads);
+  id /= c.heads;
+  const int j = int(id % slots), b = int(id / slots);
+
+  const int T_ = 1 << c.tshift;
+  int r0;
+  const int n = seq_rows(bt, b, &r0, status);
+  if (n == 0) return;
+  const int len = __ldg(bt.lens + b), start = len - n;
+  if (start < 0) {
+    if (threadIdx.x == 0) record_error(status, WQ_ERR_ARG);
+    return;
+  }
+  const int col = (start >> c.tshift) + j;
+  const int p0 = max(start, col << c.tshift), p1 = min(len, (col + 1) << c.tshift);
+  if (p0 >= p1) return;
+  const int64_t page = col < bt.width ? __ldg(bt.table + int64_t(b) * bt.width + col) : -1;
+  if (page < 0 || page >= c.pages || (rp.cos != nullptr && p1 > rp.max_pos)) {
+    if (threadIdx.x == 0) record_error(status, WQ_ERR_ARG);
+    return;
+  }
+  const int slot0 = p0 & (T_ - 1), rows = p1 - p0;
+  const int per = D >> 3;                       // pieces per row
+  const int d = int(threadIdx.x % per) * 8;
+  const int first = int(threadIdx.x) / per, rstep = int(blockDim.x) / per;
+  const T* src = (is_v ? V : K) + int64_t(r0 + (p0 - start)) * (is_v ? ldv : ldk) + int64_t(h) * D;
+  const int64_t ld = is_v ? ldv : ldk;
+  const int64_t blk = c.block(page, h);
+  uint8_t* codes = (is_v ? c.vq : c.kq) + (blk << c.tshift) * D;
+  float* sp = (is_v ? c.vs : c.ks) + blk;
+  Rope rot = rp;
+  if (is_v) rot.cos = nullptr;
+
+  // the new rows, NaN as 0; infinities keep their sign and saturate
+  float x[STEPS][8];
+  float m = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = first + i * rstep;
+    if (r >= rows) break;
+    rotated8(src + int64_t(r) * ld, d, p0 + r, rot, x[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = fabsf(x[i][e]);
+      if (a <= 3.4028234663852886e38f) {
+        m = fmaxf(m, a);
+      } else {
+        bad = true;
+        if (a != a) x[i][e] = 0.f;
+      }
+    }
+  }
+  const float old = slot0 ? *sp : 0.f;
+  m = warp_max(m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();  // also: `old` has been read by every thread
+  for (int w = 0; w < int(blockDim.x >> 5); ++w) m = fmaxf(m, red[w]);
+  float s = fmaxf(div_rn(m, TOP), 1e-8f);
+  if (slot0) s = fmaxf(s, old);
+  if (threadIdx.x == 0) *sp = s;
+  if (slot0 && s != old) {
+    const float ratio = div_rn(old, s);
+    for (int i = int(threadIdx.x) * 4; i < slot0 * D; i += int(blockDim.x) * 4) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + i);
+      uint32_t o = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t byte = (w >> (8 * e)) & 0xFFu;
+        uint32_t y;
+        if (FMT == WQ_W8_INT8) {
+          const float v = rintf(float(int8_t(byte)) * ratio);
+          y = uint32_t(int(fminf(fmaxf(v, -127.f), 127.f))) & 0xFFu;
+        } else {
+          __nv_fp8_e4m3 f;
+          f.__x = __nv_fp8_storage_t(byte);
+          y = __nv_cvt_float_to_fp8(float(f) * ratio, __NV_SATFINITE, __NV_E4M3);
+        }
+        o |= y << (8 * e);
+      }
+      *reinterpret_cast<uint32_t*>(codes + i) = o;
+    }
+  }
+  const float inv = rcp_approx(s), top = s * TOP;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = first + i * rstep;
+    if (r >= rows) break;
+    uint32_t o[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = fminf(fmaxf(x[i][e], -top), top);
+      uint32_t y;
+      if (FMT == WQ_W8_INT8)
+        y = uint32_t(uint8_t(code_i8_exact(v, s, inv)));
+      else
+        y = __nv_cvt_float_to_fp8(quot_e4m3(v, s, inv), __NV_SATFINITE, __NV_E4M3);
+      o[e >> 2] |= y << (8 * (e & 3));
+    }
+    *reinterpret_cast<uint2*>(codes + int64_t(slot0 + r) * D + d) = make_uint2(o[0], o[1]);
+  }
+  if (bad) record_error(status, WQ_ERR_NONFINITE);
+}
+
+}  // namespace kv8
+}  // namespace wq
+
+namespace wq_host {
+
+int launch_kv8_append(const void* K, const void* V, int dtype, int64_t ldk, int64_t ldv,
+                      const Kv8& a, int max_pos, cudaStream_t s) {
+  using namespace wq::kv8;
+  const int T = a.page;
+  int tshift = 0;
+  while ((1 << tshift) < T) ++tshift;
+  const Cache c{static_cast<uint8_t*>(a.kq), a.ks, static_cast<uint8_t*>(a.vq), a.vs, a.pages,
+                int(a.kv_heads), tshift};
+  const Batch bt{a.table, a.cu, a.lens, int(a.B), int(a.width), int(a.rows), int(a.max_new)};
+  const Rope rp{a.cos, a.sin, int(a.rot), max_pos, a.interleaved};
+  const int slots = int((a.max_new + T - 2) / T + 1);
+  const int64_t blocks = int64_t(a.B) * slots * a.kv_heads * 2;
+  if (blocks > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
+  const int threads = int(T * a.D / 64) < 32 ? 32 : int(T * a.D / 64);
+  const unsigned grid = unsigned(blocks);
+#define WQ_APPEND(TYPE, FMT)                                                              \
+  kv8_append_kernel<TYPE, FMT><<<grid, threads, 0, s>>>(                                  \
+      static_cast<const TYPE*>(K), static_cast<const TYPE*>(V), ldk, ldv, int(a.D), c, bt, rp, \
+      slots, status_ptr())
+  const bool i8 = a.fmt == WQ_W8_INT8;
+  if (dtype == WQ_F32) {
+    if (i8) WQ_APPEND(float, WQ_W8_INT8);
+    else WQ_APPEND(float, WQ_W8_E4M3);
+  } else if (dtype == WQ_BF16) {
+    if (i8) WQ_APPEND(__nv_bfloat16, WQ_W8_INT8);
+    else WQ_APPEND(__nv_bfloat16, WQ_W8_E4M3);
+  } else {
+    if (i8) WQ_APPEND(__half, WQ_W8_INT8);
+    else WQ_APPEND(__half, WQ_W8_E4M3);
+  }
+#undef WQ_APPEND
+  WQ_LAUNCH_CHECK("kv8_append_kernel");
+  return WQ_OK;
+}
+
+}  // namespace wq_host

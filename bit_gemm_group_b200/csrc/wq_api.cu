@@ -415,6 +415,118 @@ int wq_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, const
                                         ws, as_stream(stream));
 }
 
+// ------------------------------------------------------ paged 8-bit KV cache
+
+// What the append and the attention ask of their common arguments; `empty` is
+// set where there is nothing to do.
+static int check_kv8(int64_t n, int64_t kv_heads, int64_t D, int fmt, const void* kq,
+                     const void* ks, const void* vq, const void* vs, int64_t pages,
+                     int64_t page_size, const void* table, int64_t width, const void* cu,
+                     const void* lens, int64_t B, int64_t max_new, const void* cos,
+                     const void* sin, int64_t rot, int64_t max_pos, int interleaved,
+                     bool* empty) {
+  *empty = false;
+  if (n < 0 || kv_heads < 0 || pages < 0 || width < 0 || B < 0 || max_new < 0) return WQ_ERR_ARG;
+  if (fmt != WQ_W8_INT8 && fmt != WQ_W8_E4M3) return WQ_ERR_ARG;
+  if (interleaved != 0 && interleaved != 1) return WQ_ERR_ARG;
+  if (D != 64 && D != 128 && D != 256) return WQ_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return WQ_ERR_UNSUPPORTED;
+  if ((cos == nullptr) != (sin == nullptr)) return WQ_ERR_ARG;
+  if (cos != nullptr) {
+    if (rot <= 0 || rot > D || max_pos < 0) return WQ_ERR_ARG;
+    if ((rot % 16) != 0) return WQ_ERR_ALIGN;
+    if (!aligned16(cos) || !aligned16(sin)) return WQ_ERR_ALIGN;
+    if (max_pos > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
+  }
+  if (kv_heads > 65535 || B > (1 << 24) || n > 0x7fffffff || width * page_size > 0x7fffffff ||
+      width > 0x7fffffff || pages > 0x7fffffff)
+    return WQ_ERR_UNSUPPORTED;
+  if (n == 0 || B == 0 || kv_heads == 0 || max_new == 0) {
+    *empty = true;
+    return WQ_OK;
+  }
+  if (!kq || !ks || !vq || !vs || !table || !cu || !lens) return WQ_ERR_ARG;
+  if (!aligned16(kq) || !aligned16(ks) || !aligned16(vq) || !aligned16(vs) || !aligned16(table) ||
+      !aligned16(cu) || !aligned16(lens))
+    return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
+int wq_kv8_append(const void* K, const void* V, int dtype, int64_t n, int64_t ldk, int64_t ldv,
+                  int64_t kv_heads, int64_t D, int fmt, void* kq, void* ks, void* vq, void* vs,
+                  int64_t pages, int64_t page_size, const void* block_table, int64_t table_width,
+                  const void* cu_rows, const void* seq_lens, int64_t B, int64_t max_new,
+                  const void* cos, const void* sin, int64_t rot_dim, int64_t max_pos,
+                  int interleaved, void* stream) {
+  if (dtype != WQ_F32 && dtype != WQ_BF16 && dtype != WQ_F16) return WQ_ERR_ARG;
+  bool empty;
+  int st = check_kv8(n, kv_heads, D, fmt, kq, ks, vq, vs, pages, page_size, block_table,
+                     table_width, cu_rows, seq_lens, B, max_new, cos, sin, rot_dim, max_pos,
+                     interleaved, &empty);
+  if (st != WQ_OK || empty) return st;
+  if (!K || !V) return WQ_ERR_ARG;
+  const int64_t per16 = dtype == WQ_F32 ? 4 : 8;
+  if (ldk < kv_heads * D || ldv < kv_heads * D) return WQ_ERR_ARG;
+  if (!aligned16(K) || !aligned16(V) || (ldk % per16) != 0 || (ldv % per16) != 0)
+    return WQ_ERR_ALIGN;
+  st = wq_host::ensure_device();
+  if (st != WQ_OK) return st;
+  const wq_host::Kv8 a{kq, vq, static_cast<float*>(ks), static_cast<float*>(vs), fmt, pages,
+                       kv_heads, page_size, D, static_cast<const int*>(block_table),
+                       static_cast<const int*>(cu_rows), static_cast<const int*>(seq_lens), B,
+                       table_width, n, max_new < n ? max_new : n, static_cast<const float*>(cos),
+                       static_cast<const float*>(sin), cos ? rot_dim : 0, interleaved != 0};
+  return wq_host::launch_kv8_append(K, V, dtype, ldk, ldv, a, int(max_pos), as_stream(stream));
+}
+
+size_t wq_attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                   int64_t max_new) {
+  if (B <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || D <= 0 || max_new <= 0)
+    return 0;
+  wq_host::ensure_device();  // the size depends on the device's SM count
+  return wq_host::attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new);
+}
+
+int wq_attn_kv8(const void* Q, int dtype, int64_t n, int64_t ldq, int64_t heads, int64_t kv_heads,
+                int64_t D, int fmt, const void* kq, const void* ks, const void* vq,
+                const void* vs, int64_t pages, int64_t page_size, const void* block_table,
+                int64_t table_width, const void* cu_rows, const void* seq_lens, int64_t B,
+                int64_t max_new, const void* cos, const void* sin, int64_t rot_dim,
+                int64_t max_pos, int interleaved, float scale, void* out, void* ws,
+                size_t ws_bytes, void* stream) {
+  if (dtype != WQ_BF16 && dtype != WQ_F16) return WQ_ERR_ARG;
+  if (heads < 0) return WQ_ERR_ARG;
+  bool empty;
+  int st = check_kv8(n, kv_heads, D, fmt, kq, ks, vq, vs, pages, page_size, block_table,
+                     table_width, cu_rows, seq_lens, B, max_new, cos, sin, rot_dim, max_pos,
+                     interleaved, &empty);
+  if (st != WQ_OK || empty) return st;
+  if (!(scale > 0.f && scale <= 3.0e38f)) return WQ_ERR_ARG;
+  if (heads == 0 || heads % kv_heads != 0) return WQ_ERR_ARG;
+  if (max_new > n) max_new = n;
+  if (heads > 65535 || max_new * (heads / kv_heads) > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
+  if (!Q || !out) return WQ_ERR_ARG;
+  if (ldq < heads * D) return WQ_ERR_ARG;
+  if (!aligned16(Q) || !aligned16(out) || (ldq % 8) != 0 ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return WQ_ERR_ALIGN;
+  if (!ws) return WQ_ERR_WORKSPACE;
+  st = wq_host::ensure_device();
+  if (st != WQ_OK) return st;
+  if (ws_bytes < wq_host::attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new))
+    return WQ_ERR_WORKSPACE;
+  const wq_host::Kv8 a{const_cast<void*>(kq), const_cast<void*>(vq),
+                       static_cast<float*>(const_cast<void*>(ks)),
+                       static_cast<float*>(const_cast<void*>(vs)), fmt, pages, kv_heads,
+                       page_size, D, static_cast<const int*>(block_table),
+                       static_cast<const int*>(cu_rows), static_cast<const int*>(seq_lens), B,
+                       table_width, n, max_new < n ? max_new : n, static_cast<const float*>(cos),
+                       static_cast<const float*>(sin), cos ? rot_dim : 0, interleaved != 0};
+  return wq_host::launch_attn_kv8(Q, dtype, ldq, heads, a, int(max_pos), scale, out, ws,
+                                  as_stream(stream));
+}
+
 // -------------------------------------------------------------------- GPTQ
 
 size_t wq_gptq_workspace_bytes(int64_t N, int64_t K) {

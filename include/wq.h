@@ -65,6 +65,9 @@ typedef enum {
 
 typedef enum { WQ_F32 = 0, WQ_BF16 = 1, WQ_F16 = 2 } wq_dtype;
 
+/* 8-bit formats of weights (wq_gemm_w8a16) and of the paged KV cache */
+enum { WQ_W8_INT8 = 0, WQ_W8_E4M3 = 1 };
+
 /*
  * wq_quantize_pack -- quantize a weight matrix W [N, K].
  *
@@ -282,6 +285,82 @@ WQ_API int wq_quant_kv(const void *K, const void *V, int dtype, int64_t BH, int6
                        int64_t D, void *qk, void *sk, void *qv, void *sv, void *stream);
 
 /*
+ * Paged 8-bit KV cache ([P4] sec. 6: the cache in 8 bits; pages so that
+ * sequences of different lengths share one allocation).  One scale for each
+ * block of tokens (a page) and kv head, keys and values apart:
+ *   kq, vq : codes [pages, kv_heads, page_size, D], fmt WQ_W8_INT8 (int8) or
+ *            WQ_W8_E4M3 (E4M3)
+ *   ks, vs : fp32 [pages, kv_heads]; a value is code * scale
+ *   block_table : int32 [B, table_width]; position p of sequence b is slot
+ *            p % page_size of page block_table[b, p / page_size]
+ *   cu_rows  : int32 [B + 1], the rows of sequence b are [cu_rows[b],
+ *            cu_rows[b + 1]) of the call's n rows, at most max_new of them
+ *   seq_lens : int32 [B], positions of the sequence INCLUDING the call's rows,
+ *            so that row i of its m rows is at position seq_lens[b] - m + i.
+ *            The append and the attention of a step take the same cu_rows and
+ *            seq_lens.
+ *   cos, sin : fp32 [max_pos, rot_dim / 2], or both NULL for no rotation: the
+ *            first rot_dim elements of a head are rotated by their position's
+ *            angles, in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ *            interleaved; (a, b) -> (a cos - b sin, b cos + a sin) in fp32.
+ * D 64, 128 or 256, page_size 16, 32, 64 or 128 (others: WQ_ERR_UNSUPPORTED),
+ * rot_dim % 16 == 0.  Tensors are 16-byte aligned; rows of K, V and Q are
+ * ldk, ldv, ldq elements apart (multiples of 16 bytes), the heads of a row
+ * contiguous.  What the kernels find wrong in the tables (a page outside the
+ * cache, a position outside the table or the angles, cu_rows out of order or
+ * a sequence with more rows than max_new) is reported as WQ_ERR_ARG in the
+ * device status; nothing outside the tensors is touched.
+ *
+ * wq_kv8_append -- write K, V [n, kv_heads, D] (dtype WQ_F32 / WQ_BF16 /
+ * WQ_F16), K rotated.  For each page and head that receives rows
+ *   s' = max(max |x| of its new rows / qmax, 1e-8), qmax 127 or 448, and at
+ *        least the block's scale s if older rows of the sequence lie in front
+ *        of them in the page (a page's scale grows only; a page that starts
+ *        with a new row starts anew);
+ *   older codes c become round(c * (s / s')) where s' > s, new codes are
+ *   round(x / s') (IEEE fp32, half to even, saturating).
+ * Slots behind the last new row keep their bytes.  Infinities saturate, NaN
+ * becomes 0, neither counts for the scale, so that one bad row does not cost a
+ * page its older rows; the status reports WQ_ERR_NONFINITE.  A sequence with
+ * an error in its tables is skipped (a page of it, where only that is wrong).
+ * The pages that one call writes must be distinct.
+ */
+WQ_API int wq_kv8_append(const void *K, const void *V, int dtype, int64_t n, int64_t ldk,
+                         int64_t ldv, int64_t kv_heads, int64_t D, int fmt, void *kq, void *ks,
+                         void *vq, void *vs, int64_t pages, int64_t page_size,
+                         const void *block_table, int64_t table_width, const void *cu_rows,
+                         const void *seq_lens, int64_t B, int64_t max_new, const void *cos,
+                         const void *sin, int64_t rot_dim, int64_t max_pos, int interleaved,
+                         void *stream);
+
+/*
+ * wq_attn_kv8 -- causal attention of Q [n, heads, D] (dtype WQ_BF16 / WQ_F16,
+ * rotated on the way like K) over the cache; query head h reads kv head
+ * h / (heads / kv_heads).  Row i of a sequence's m rows sees the positions
+ * j <= seq_lens[b] - m + i:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  out [n, heads, D] of dtype.
+ * Scores, maxima and sums are fp32; the codes and the weights meet the tensor
+ * cores as f16 (the codes exactly, a weight relative to its row's maximum).  A
+ * row that sees no position gives zeros.  Rows of no sequence are left as they
+ * were.  Positions whose page is outside the cache are left out (and
+ * reported); a row at a position without angles is not rotated (and reported).
+ * Codes and scales of positions that a row does not see, and bytes of slots
+ * nobody wrote, do not reach its result.
+ * ws: wq_attn_kv8_workspace_bytes(...) bytes on the current device, 256-byte
+ * aligned, any contents; calls that may overlap on the GPU need separate
+ * workspaces.  Results do not depend on timing.
+ */
+WQ_API size_t wq_attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                          int64_t max_new);
+WQ_API int wq_attn_kv8(const void *Q, int dtype, int64_t n, int64_t ldq, int64_t heads,
+                       int64_t kv_heads, int64_t D, int fmt, const void *kq, const void *ks,
+                       const void *vq, const void *vs, int64_t pages, int64_t page_size,
+                       const void *block_table, int64_t table_width, const void *cu_rows,
+                       const void *seq_lens, int64_t B, int64_t max_new, const void *cos,
+                       const void *sin, int64_t rot_dim, int64_t max_pos, int interleaved,
+                       float scale, void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * FP8 E4M3 W8A8 ([P4] sec. 2.3 names FP8 E4M3 as the 8-bit float format of
  * the newest tensor cores; the recipe is the W8A8 one with E4M3 in place of
  * int8).  E4M3: 1 sign, 4 exponent bits (bias 7), 3 mantissa bits, largest
@@ -315,7 +394,6 @@ WQ_API int wq_quantize_fp8_rows(const void *A, int a_dtype, int64_t R, int64_t K
  * most 2^-13 of it; a chunk of X holding a NaN or an infinity is multiplied
  * in fp32).  Requires K % 64 == 0; all pointers 16-byte aligned.
  */
-enum { WQ_W8_INT8 = 0, WQ_W8_E4M3 = 1 };
 WQ_API int wq_gemm_w8a16(const void *X, int64_t M, int64_t K, const void *Wq, int w_fmt,
                          const void *w_scales, int64_t N, void *Y, void *stream);
 
