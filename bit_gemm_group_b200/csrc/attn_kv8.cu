@@ -5,11 +5,13 @@
 //   s_j = scale (rope(q) . kq_j) ks(page of j),  j <= len - n + i
 //   o   = sum_j softmax(s)_j vq_j vs(page of j)
 //
-// Bound by HBM: every code is read once per block of RB rows (8 or 16), 2 D
-// bytes per position and head.  The codes go to f16 (exactly: int8 and E4M3
-// are subsets) and through mma.sync m16n8k16; at one row block per code byte
-// that needs about a tenth of the rate that the memory can feed, so the
-// tensor memory's hand-offs would only add latency here.
+// Bound by HBM: every code is read once per block of 8 rows, 2 D bytes per
+// position and head.  The codes go to f16 (exactly: int8 and E4M3 are subsets)
+// and through mma.sync m16n8k16.  The scores' products have 16 rows for 8
+// queries: rows 0 to 7 hold the rotated query rounded to f16, rows 8 to 15 what
+// that rounding left, so that the query counts with 22 bits at no cost.  A
+// decode step needs about a third of the mma.sync rate while it streams at the
+// copy rate, so tensor memory would add hand-offs and no speed.
 //
 // Work is cut into units of TK positions of one (sequence, head, row block),
 // numbered with the position fastest, and every warp of the grid takes an
@@ -33,7 +35,8 @@
 namespace wq {
 namespace kv8 {
 
-constexpr int WARPS = 8;
+constexpr int MAX_WARPS = 12;
+constexpr int RB = 8;      // rows per block
 constexpr float LAG = 8.f;  // how far the maximum may grow before the sums are rescaled
 constexpr float OFF = 6.f;
 
@@ -41,7 +44,9 @@ template <int D_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr int TK = D == 256 ? 16 : 32;    // positions per unit
-  static constexpr int STAGES = D == 64 ? 5 : 3;
+  // a 256-wide head's sums need the registers of 8 warps per SM
+  static constexpr int WARPS = D == 256 ? 8 : MAX_WARPS;
+  static constexpr int STAGES = D == 128 ? 2 : 3;
   // rows of 128 bytes and more are kept as 16-byte pieces XORed with the row
   // (conflict-free fragment reads); 64-byte value rows are 80 bytes apart
   static constexpr int KP = D, VP = D == 64 ? 80 : D;
@@ -57,6 +62,12 @@ __device__ __forceinline__ int swz(int D, int row, int piece) {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same, or 16 zero bytes
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -90,32 +101,48 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Codes as f16 pairs.  int8: the byte with its top bit flipped is u = c + 128;
-// 0x6400 | u is 1024 + u in f16, minus 1152 gives c.  E4M3: sign, then exponent
-// and mantissa one bit lower, is c 2^-8 in f16 (subnormals too); the 2^8 is in
-// the caller's scale.  Every byte gives a finite value, so that slots nobody
-// wrote cannot reach a result through their zero weights.
+// Codes as f16 pairs, exactly.
+// Keys: int8 as u = c + 128 in the subnormals (u 2^-24); the score of -128
+//   ones is where a row's sum starts.  E4M3 through the hardware conversion.
+// Values: int8 as 0x6400 | u, which is 1024 + u, minus 1152 (a bias of 128 per
+//   weight would swamp a long sum whose values cancel).
 template <int FMT>
-struct Code {
-  static constexpr float SCALE = FMT == WQ_W8_INT8 ? 1.f : 256.f;
-  // the halves of t hold a code in both of their bytes
-  static __device__ __forceinline__ uint32_t halves(uint32_t t) {
-    if (FMT == WQ_W8_INT8) {
-      const uint32_t u = (t & 0x00FF00FFu) ^ 0x64806480u;
-      uint32_t r;
-      asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
-      return r;
-    }
-    return (t & 0x80008000u) | ((t >> 1) & 0x3F803F80u);
+struct Code;
+template <>
+struct Code<WQ_W8_INT8> {
+  static constexpr float KEY = 16777216.f, BIAS = 128.f / 16777216.f;
+  // codes 0, 1 (a) and 2, 3 (b) of a word of keys
+  static __device__ __forceinline__ void key(uint32_t w, uint32_t& a, uint32_t& b) {
+    const uint32_t x = w ^ 0x80808080u;
+    a = __byte_perm(x, 0, 0x4140);
+    b = __byte_perm(x, 0, 0x4342);
   }
-  // codes 0, 1 (a) and 2, 3 (b) of a word
-  static __device__ __forceinline__ void word(uint32_t w, uint32_t& a, uint32_t& b) {
-    a = halves(__byte_perm(w, 0, 0x1100));
-    b = halves(__byte_perm(w, 0, 0x3322));
+  // codes 2 e and 2 e + 1 of two words of values, each as a pair
+  static __device__ __forceinline__ void value(uint32_t w0, uint32_t w1, int e, uint32_t& a,
+                                               uint32_t& b) {
+    const uint32_t u = (__byte_perm(w0, w1, 0x4400 + 0x2222 * e) & 0x00FF00FFu) ^ 0x64806480u;
+    const uint32_t v = (__byte_perm(w0, w1, 0x5511 + 0x2222 * e) & 0x00FF00FFu) ^ 0x64806480u;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(a) : "r"(u), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(b) : "r"(v), "r"(0x64806480u));
   }
-  // code e of two words
-  static __device__ __forceinline__ uint32_t cross(uint32_t w0, uint32_t w1, int e) {
-    return halves(__byte_perm(w0, w1, 0x4400 + 0x1111 * e));
+};
+template <>
+struct Code<WQ_W8_E4M3> {
+  static constexpr float KEY = 1.f, BIAS = 0.f;
+  static __device__ __forceinline__ void pairs(uint32_t w, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  }
+  static __device__ __forceinline__ void key(uint32_t w, uint32_t& a, uint32_t& b) {
+    pairs(w, a, b);
+  }
+  static __device__ __forceinline__ void value(uint32_t w0, uint32_t w1, int e, uint32_t& a,
+                                               uint32_t& b) {
+    pairs(__byte_perm(w0, w1, 0x5140 + 0x2222 * e), a, b);
   }
 };
 
@@ -150,8 +177,7 @@ struct Cursor {
   int b, h, rb, tile;           // sequence, kv head, row block, unit of positions
   int n, q0, len, tiles, nrb;   // of sequence b
 
-  __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int RB, int TK,
-                                       int* status) {
+  __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int TK, int* status) {
     n = seq_rows(bt, b, &q0, status);
     len = __ldg(bt.lens + b);
     const int64_t most = int64_t(bt.width) << tshift;
@@ -176,12 +202,12 @@ struct Args {
   int64_t* prefix;   // [B + 1] first unit of each sequence
 };
 
-template <typename TQ, int FMT, int D, int NB>
-__global__ void __launch_bounds__(WARPS * 32, 1)
+template <typename TQ, int FMT, int D>
+__global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     attn_kv8_kernel(const TQ* __restrict__ Q, TQ* __restrict__ O, Cache c, Batch bt, Rope rp,
                     Args ar, int* status) {
   using S = Shape<D>;
-  constexpr int RB = 8 * NB, TK = S::TK, NT = TK / 8, MT = D / 16;
+  constexpr int WARPS = S::WARPS, TK = S::TK, NT = TK / 8, MT = D / 16;
   constexpr int KS = D / 16;  // steps of the product over D
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t warp_sum[WARPS], start_at[WARPS], run_at[WARPS];
@@ -202,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       s.b = b0 + int(threadIdx.x);
       int64_t mine = 0;
       if (s.b < bt.B) {
-        s.load(bt, c.tshift, ar.G, RB, TK, pass ? nullptr : status);
+        s.load(bt, c.tshift, ar.G, TK, pass ? nullptr : status);
         mine = s.units(c.heads);
       }
       int64_t inc = mine;
@@ -252,7 +278,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   u0 = run_start(id, U, W);
   u1 = run_start(id + 1, U, W);
   me.b = start_b[warp];
-  me.load(bt, c.tshift, ar.G, RB, TK, nullptr);
+  me.load(bt, c.tshift, ar.G, TK, nullptr);
   {
     const int64_t at = start_at[warp];
     me.tile = int(at % me.tiles);
@@ -270,7 +296,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     do {
       ++s.b;
       if (s.b >= bt.B) return;
-      s.load(bt, c.tshift, ar.G, RB, TK, nullptr);
+      s.load(bt, c.tshift, ar.G, TK, nullptr);
     } while (s.n == 0);
   };
 
@@ -311,18 +337,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
           }
         }
       }
-      constexpr int PER = D / 16, STEP = 32 / PER > 0 ? 32 / PER : 1;
-      const int piece = lane % PER;
+      // rows are contiguous in a page, so a lane's pieces are 512 bytes apart
+      constexpr int PER = D / 16, STEP = 32 / PER, COPIES = TK / STEP;
+      const int rows = ahead.len - tok0, r0 = lane / PER, piece = lane % PER;
+      const int64_t at0 = ((c.block(ok0 ? pg0 : 0, ahead.h) << c.tshift) + (tok0 & (T_ - 1))) * D + lane * 16;
+      const int64_t at1 =
+          T_ < TK ? (c.block(ok1 ? pg1 : 0, ahead.h) << c.tshift) * D + lane * 16 - 16 * D : at0;
 #pragma unroll
-      for (int r0 = 0; r0 < TK; r0 += STEP) {
-        const int r = r0 + lane / PER, tok = tok0 + r;
-        const bool second = (tok >> c.tshift) != col;
-        if (tok < ahead.len && (second ? ok1 : ok0)) {
-          const int64_t at = ((c.block(second ? pg1 : pg0, ahead.h) << c.tshift) + (tok & (T_ - 1))) * D +
-                             piece * 16;
-          cp16(st + r * S::KP + swz(D, r, piece) * 16, c.kq + at);
-          cp16(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, c.vq + at);
-        }
+      for (int i = 0; i < COPIES; ++i) {
+        const int r = r0 + i * STEP;
+        const bool second = T_ < TK && i >= COPIES / 2;
+        const bool valid = r < rows && (second ? ok1 : ok0);
+        const int64_t at = (second ? at1 : at0) + i * 512;
+        cp16z(st + r * S::KP + swz(D, r, piece) * 16, c.kq + at, valid);
+        cp16z(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, c.vq + at, valid);
       }
       ++issued;
       advance(ahead);
@@ -333,10 +361,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 #pragma unroll
   for (int i = 0; i < S::STAGES - 1; ++i) issue();
 
-  uint32_t qa[KS][2 * NB];
-  float acc[NB][MT][4];
-  float m[NB], l[NB], fq[NB];
-  int lim[NB];
+  uint32_t qa[KS][4];
+  float acc[MT][4];
+  float m = -CUDART_INF_F, l = 0.f, fq = 0.f, start = 0.f;
+  int lim = 0;
   bool fresh = true, first_seg = true;
   int seg_tile0 = me.tile;
 
@@ -345,14 +373,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       // -------------------------------------------- a segment's queries
       fresh = false;
       seg_tile0 = me.tile;
+      constexpr int P = D / 8, RPP = 32 / P;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        constexpr int P = D / 8, RPP = 32 / P;
+      for (int part = 0; part < 2; ++part) {  // rounded to f16, then what that left
         __syncwarp();
 #pragma unroll 1
-        for (int r0 = 0; r0 < 8; r0 += RPP) {
+        for (int r0 = 0; r0 < RB; r0 += RPP) {
           const int r = r0 + lane / P, d = (lane % P) * 8;
-          const int rr = me.rb * RB + nb * 8 + r;
+          const int rr = me.rb * RB + r;
           float x[8] = {};
           if (rr < me.n * ar.G) {
             const int i = rr / ar.G;
@@ -378,15 +406,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                        : 0;
           ex = ex > 100 ? 100 : ex;
           const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] *= up;
+            sum += x[e];
+            if (part) x[e] -= __half2float(__float2half_rn(x[e]));
+          }
           uint4 o;
-          o.x = f16x2(x[0] * up, x[1] * up);
-          o.y = f16x2(x[2] * up, x[3] * up);
-          o.z = f16x2(x[4] * up, x[5] * up);
-          o.w = f16x2(x[6] * up, x[7] * up);
+          o.x = f16x2(x[0], x[1]);
+          o.y = f16x2(x[2], x[3]);
+          o.z = f16x2(x[4], x[5]);
+          o.w = f16x2(x[6], x[7]);
           *reinterpret_cast<uint4*>(qs + r * S::QP + d) = o;
-          if (lane % P == 0)
-            *reinterpret_cast<float*>(qs + r * S::QP + D) =
-                __uint_as_float(uint32_t(127 - ex) << 23);
+          if (part == 0) {
+#pragma unroll
+            for (int q = P / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+            if (lane % P == 0)
+              *reinterpret_cast<float2*>(qs + r * S::QP + D) =
+                  make_float2(__uint_as_float(uint32_t(127 - ex) << 23), sum);
+          }
         }
         __syncwarp();
 #pragma unroll
@@ -394,19 +433,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
           const int j = ks >> 2, w = ks & 3;
           const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
           const uint2 v = lds64(qbase + uint32_t(g * S::QP + pc * 16 + w * 4) * 2);
-          qa[ks][nb] = v.x;
-          qa[ks][NB + nb] = v.y;
+          qa[ks][part] = v.x;
+          qa[ks][2 + part] = v.y;
         }
-        fq[nb] = lds32f(qbase + uint32_t(g * S::QP + D) * 2) * ar.scale_log2 * Code<FMT>::SCALE;
-        const int rr = me.rb * RB + nb * 8 + g;
-        lim[nb] = rr < me.n * ar.G ? min(me.len, me.len - me.n + rr / ar.G + 1) : 0;
-        m[nb] = -CUDART_INF_F;
-        l[nb] = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nb][mt][e] = 0.f;
+        if (part == 0) {
+          fq = lds32f(qbase + uint32_t(g * S::QP + D) * 2) * ar.scale_log2 * Code<FMT>::KEY;
+          start = -Code<FMT>::BIAS * lds32f(qbase + uint32_t(g * S::QP + D) * 2 + 4);
+        }
       }
+      const int rr = me.rb * RB + g;
+      lim = rr < me.n * ar.G ? min(me.len, me.len - me.n + rr / ar.G + 1) : 0;
+      m = -CUDART_INF_F;
+      l = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
     }
     cp_wait<S::STAGES - 2>();
     __syncwarp();
@@ -417,9 +459,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // -------------------------------------------------- scores
     float sc[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      sc[nt][0] = sc[nt][1] = start;
+      sc[nt][2] = sc[nt][3] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
@@ -431,10 +474,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t b0, b1;
-          Code<FMT>::word(kw[w], b0, b1);
+          Code<FMT>::key(kw[w], b0, b1);
           const int ks = j * 4 + w;
-          mma16816(sc[nt], qa[ks][0], NB == 2 ? qa[ks][NB - 1] : 0u, qa[ks][NB],
-                   NB == 2 ? qa[ks][2 * NB - 1] : 0u, b0, b1);
+          mma16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
         }
       }
     }
@@ -444,113 +486,83 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (T_ < TK) {
       k1 = lds32f(scb + 8);
       v1 = lds32f(scb + 12);
-      if ((((me.tile * TK) >> c.tshift) + 1) << c.tshift >= me.len) k1 = 0.f, v1 = -1.f;
+      if (((((me.tile * TK) >> c.tshift) + 1) << c.tshift) >= me.len) k1 = 0.f, v1 = -1.f;
     }
     const float lv0 = v0 < 0.f ? -CUDART_INF_F : __log2f(fmaxf(v0, 1e-30f));
     const float lv1 = v1 < 0.f ? -CUDART_INF_F : __log2f(fmaxf(v1, 1e-30f));
     const float rv0 = __fdividef(1.f, fmaxf(v0, 1e-30f)), rv1 = __fdividef(1.f, fmaxf(v1, 1e-30f));
-    float mx[NB];
+    const float f0 = fq * k0, f1 = fq * k1;
+    float mx = -CUDART_INF_F;
+    const bool edge = __any_sync(0xffffffffu, (me.tile + 1) * TK > lim);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float f0 = fq[nb] * k0, f1 = fq[nb] * k1;
-      mx[nb] = -CUDART_INF_F;
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool hi = NT == 4 && nt >= 2;  // the unit's second page, where it has two
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const bool hi = NT == 4 && nt >= 2;  // the unit's second page, where it has two
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = sc[nt][2 * nb + e];
-          x = fmaf(x, hi ? f1 : f0, hi ? lv1 : lv0);
-          if (me.tile * TK + nt * 8 + 2 * t + e >= lim[nb]) x = -CUDART_INF_F;
-          mx[nb] = fmaxf(mx[nb], x);
-        }
-      }
-      mx[nb] = fmaxf(mx[nb], __shfl_xor_sync(0xffffffffu, mx[nb], 1));
-      mx[nb] = fmaxf(mx[nb], __shfl_xor_sync(0xffffffffu, mx[nb], 2));
-    }
-    bool grow = mx[0] > m[0] + LAG;
-    if (NB == 2) grow |= mx[NB - 1] > m[NB - 1] + LAG;
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const float now = fmaxf(m[nb], mx[nb]);
-        const float al = now == m[nb] ? 1.f : exp2_approx(m[nb] - now);
-        m[nb] = now;
-        l[nb] *= al;
-        const float a0 = __shfl_sync(0xffffffffu, al, t * 8);
-        const float a1 = __shfl_sync(0xffffffffu, al, t * 8 + 4);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          acc[nb][mt][0] *= a0;
-          acc[nb][mt][1] *= a1;
-          acc[nb][mt][2] *= a0;
-          acc[nb][mt][3] *= a1;
-        }
+      for (int e = 0; e < 2; ++e) {
+        float& x = sc[nt][e];
+        x = fmaf(x + sc[nt][2 + e], hi ? f1 : f0, hi ? lv1 : lv0);
+        if (edge && me.tile * TK + nt * 8 + 2 * t + e >= lim) x = -CUDART_INF_F;
+        mx = fmaxf(mx, x);
       }
     }
-    uint32_t pb[NB][NT];
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    if (__any_sync(0xffffffffu, mx > m + LAG)) {
+      const float now = fmaxf(m, mx);
+      const float al = now == m ? 1.f : exp2_approx(m - now);
+      m = now;
+      l *= al;
+      const float a0 = __shfl_sync(0xffffffffu, al, t * 8);
+      const float a1 = __shfl_sync(0xffffffffu, al, t * 8 + 4);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float off = OFF - (m[nb] == -CUDART_INF_F ? 0.f : m[nb]);
+      for (int mt = 0; mt < MT; ++mt) {
+        acc[mt][0] *= a0;
+        acc[mt][1] *= a1;
+        acc[mt][2] *= a0;
+        acc[mt][3] *= a1;
+      }
+    }
+    uint32_t pb[NT];
+    {
+      const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float a = exp2_approx(sc[nt][2 * nb] + off);
-        const float b = exp2_approx(sc[nt][2 * nb + 1] + off);
+        const float a = exp2_approx(sc[nt][0] + off), b = exp2_approx(sc[nt][1] + off);
         if (NT == 4 && nt >= 2)
           s1 += a + b;
         else
           s0 += a + b;
-        pb[nb][nt] = f16x2(a, b);
+        pb[nt] = f16x2(a, b);
       }
-      l[nb] += s0 * rv0 + s1 * rv1;
+      l += s0 * rv0 + s1 * rv1;
     }
 
     // -------------------------------------------------- values
 #pragma unroll
     for (int ks = 0; ks < TK / 16; ++ks) {
       const int r = ks * 16 + 2 * t;
-      if (D == 64) {
-        const int pc = g >> 1, off = (g & 1) * 8;
-        const uint2 x0 = lds64(vb + r * S::VP + pc * 16 + off);
-        const uint2 x1 = lds64(vb + (r + 1) * S::VP + pc * 16 + off);
-        const uint2 x8 = lds64(vb + (r + 8) * S::VP + pc * 16 + off);
-        const uint2 x9 = lds64(vb + (r + 9) * S::VP + pc * 16 + off);
-        const uint32_t w0[2] = {x0.x, x0.y}, w1[2] = {x1.x, x1.y};
-        const uint32_t w8[2] = {x8.x, x8.y}, w9[2] = {x9.x, x9.y};
+      constexpr int WORDS = D == 64 ? 2 : 4;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int w = mt >> 1 & 1, e = (mt & 1) * 2;
-          const uint32_t a0 = Code<FMT>::cross(w0[w], w1[w], e);
-          const uint32_t a1 = Code<FMT>::cross(w0[w], w1[w], e + 1);
-          const uint32_t a2 = Code<FMT>::cross(w8[w], w9[w], e);
-          const uint32_t a3 = Code<FMT>::cross(w8[w], w9[w], e + 1);
+      for (int q = 0; q < (D == 64 ? 1 : D / 128); ++q) {
+        uint32_t w[4][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma16816(acc[nb][mt], a0, a1, a2, a3, pb[nb][2 * ks], pb[nb][2 * ks + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < D / 128; ++q) {
-          const int pc = g + 8 * q;
-          const uint4 x0 = lds128(vb + r * S::VP + swz(D, r, pc) * 16);
-          const uint4 x1 = lds128(vb + (r + 1) * S::VP + swz(D, r + 1, pc) * 16);
-          const uint4 x8 = lds128(vb + (r + 8) * S::VP + swz(D, r + 8, pc) * 16);
-          const uint4 x9 = lds128(vb + (r + 9) * S::VP + swz(D, r + 9, pc) * 16);
-          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-          const uint32_t w8[4] = {x8.x, x8.y, x8.z, x8.w}, w9[4] = {x9.x, x9.y, x9.z, x9.w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int w = k >> 1, e = (k & 1) * 2;
-            const uint32_t a0 = Code<FMT>::cross(w0[w], w1[w], e);
-            const uint32_t a1 = Code<FMT>::cross(w0[w], w1[w], e + 1);
-            const uint32_t a2 = Code<FMT>::cross(w8[w], w9[w], e);
-            const uint32_t a3 = Code<FMT>::cross(w8[w], w9[w], e + 1);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816(acc[nb][(q * 8 + k) % MT], a0, a1, a2, a3, pb[nb][2 * ks],
-                       pb[nb][2 * ks + 1]);
+        for (int k = 0; k < 4; ++k) {  // positions r, r + 1, r + 8, r + 9
+          const int row = r + (k & 1) + 8 * (k >> 1);
+          if (D == 64) {
+            const uint2 x = lds64(vb + row * S::VP + g * 8);
+            w[k][0] = x.x, w[k][1] = x.y;
+          } else {
+            const uint4 x = lds128(vb + row * S::VP + swz(D, row, g + 8 * q) * 16);
+            w[k][0] = x.x, w[k][1] = x.y, w[k][2] = x.z, w[k][3] = x.w;
           }
+        }
+#pragma unroll
+        for (int k = 0; k < 2 * WORDS; ++k) {
+          uint32_t a0, a1, a2, a3;
+          Code<FMT>::value(w[0][k >> 1], w[1][k >> 1], k & 1, a0, a1);
+          Code<FMT>::value(w[2][k >> 1], w[3][k >> 1], k & 1, a2, a3);
+          mma16816(acc[q * 8 + k], a0, a1, a2, a3, pb[2 * ks], pb[2 * ks + 1]);
         }
       }
     }
@@ -560,49 +572,46 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     if (last) {
       const bool whole = seg_tile0 == 0 && me.tile + 1 == me.tiles;
       const int64_t part = id * 2 + (first_seg ? 0 : 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (!whole && t == 0) {
+        float* ml = ar.part_ml + (part * RB + g) * 2;
+        __stcg(ml, m);
+        __stcg(ml + 1, l);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 1);
-        l[nb] += __shfl_xor_sync(0xffffffffu, l[nb], 2);
-        if (!whole && t == 0) {
-          float* ml = ar.part_ml + (part * RB + nb * 8 + g) * 2;
-          __stcg(ml, m[nb]);
-          __stcg(ml + 1, l[nb]);
-        }
-        const float inv = l[nb] == 0.f ? 0.f : Code<FMT>::SCALE / l[nb];
+      for (int q = 0; q < 2; ++q) {
+        const int r = 2 * t + q;
+        const float iv = __shfl_sync(0xffffffffu, inv, t * 8 + 4 * q);
+        const int rr = me.rb * RB + r;
+        constexpr int RUN = D == 64 ? 8 : 16;  // consecutive elements of this lane
+        if (!whole) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int r = nb * 8 + 2 * t + q;
-          const float iv = __shfl_sync(0xffffffffu, inv, t * 8 + 4 * q);
-          const int rr = me.rb * RB + r;
-          constexpr int RUN = D == 64 ? 8 : 16;  // consecutive elements of this lane
-          if (!whole) {
+          for (int k = 0; k < D / 8; k += 4) {
+            float* dst = ar.parts + (part * RB + r) * D + (k / RUN) * 128 + g * RUN + k % RUN;
+            __stcg(reinterpret_cast<float4*>(dst),
+                   make_float4(acc[k / 2][q], acc[k / 2][q + 2], acc[k / 2 + 1][q],
+                               acc[k / 2 + 1][q + 2]));
+          }
+        } else if (rr < me.n * ar.G) {
+          const int i = rr / ar.G;
+          TQ* o = O + (int64_t(me.q0 + i) * ar.heads + me.h * ar.G + (rr - i * ar.G)) * D;
 #pragma unroll
-            for (int k = 0; k < D / 8; k += 4) {
-              float* dst = ar.parts + (part * RB + r) * D + (k / RUN) * 128 + g * RUN + k % RUN;
-              __stcg(reinterpret_cast<float4*>(dst),
-                     make_float4(acc[nb][k / 2][q], acc[nb][k / 2][q + 2], acc[nb][k / 2 + 1][q],
-                                 acc[nb][k / 2 + 1][q + 2]));
+          for (int k = 0; k < D / 8; k += 8) {
+            union {
+              uint4 v;
+              TQ e[8];
+            } y;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float v = acc[(k + e) / 2][q + 2 * (e & 1)] * iv;
+              if constexpr (std::is_same<TQ, __half>::value)
+                y.e[e] = __float2half_rn(v);
+              else
+                y.e[e] = __float2bfloat16_rn(v);
             }
-          } else if (rr < me.n * ar.G) {
-            const int i = rr / ar.G;
-            TQ* o = O + (int64_t(me.q0 + i) * ar.heads + me.h * ar.G + (rr - i * ar.G)) * D;
-#pragma unroll
-            for (int k = 0; k < D / 8; k += 8) {
-              union {
-                uint4 v;
-                TQ e[8];
-              } y;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float v = acc[nb][(k + e) / 2][q + 2 * (e & 1)] * iv;
-                if constexpr (sizeof(TQ) == 2 && std::is_same<TQ, __half>::value)
-                  y.e[e] = __float2half_rn(v);
-                else
-                  y.e[e] = __float2bfloat16_rn(v);
-              }
-              *reinterpret_cast<uint4*>(o + (k / RUN) * 128 + g * RUN + k % RUN) = y.v;
-            }
+            *reinterpret_cast<uint4*>(o + (k / RUN) * 128 + g * RUN + k % RUN) = y.v;
           }
         }
       }
@@ -617,11 +626,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 // Joins the parts of cut segments: one CTA per (sequence, head, row block),
 // RB x 32 threads times GROUPS; group k takes parts k, k + GROUPS, ... of its
 // row in order, and the groups are added in order.
-template <typename TQ, int FMT, int D, int NB>
+template <typename TQ, int D>
 __global__ void __launch_bounds__(1024)
     attn_kv8_join_kernel(TQ* __restrict__ O, Cache c, Batch bt, Args ar, int64_t total_warps,
                          int most_rb) {
-  constexpr int RB = 8 * NB, GROUPS = 32 / RB, PER = D / 32;  // elements per lane
+  constexpr int GROUPS = 32 / RB, PER = D / 32;  // elements per lane
   __shared__ float sm[GROUPS][RB], sl[GROUPS][RB];
   __shared__ float so[GROUPS][RB][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(1024)
   const int h = int(id % c.heads), b = int(id / c.heads);
   Cursor s;
   s.b = b;
-  s.load(bt, c.tshift, ar.G, RB, Shape<D>::TK, nullptr);
+  s.load(bt, c.tshift, ar.G, Shape<D>::TK, nullptr);
   if (s.n == 0 || rb >= s.nrb) return;
   const int64_t U = ar.prefix[bt.B], W = workers(U, total_warps);
   const int64_t f = ar.prefix[b] + (int64_t(h) * s.nrb + rb) * s.tiles;
@@ -696,7 +705,7 @@ __global__ void __launch_bounds__(1024)
   }
   const int rr = rb * RB + r;
   if (rr >= s.n * ar.G) return;
-  const float inv = l == 0.f ? 0.f : Code<FMT>::SCALE / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = rr / ar.G;
   TQ* dst = O + (int64_t(s.q0 + i) * ar.heads + h * ar.G + (rr - i * ar.G)) * D;
 #pragma unroll
@@ -717,15 +726,11 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Row blocks of 16 where there are more than 8 rows to a (sequence, head); a
-// 256-wide head's sums fit the registers of 8 rows only.
-int row_blocks(int64_t max_rows, int64_t D) { return max_rows > 8 && D <= 128 ? 2 : 1; }
-
 struct Ws {
   size_t ml, prefix, bytes;
 };
-Ws attn_ws(int64_t B, int64_t max_rows, int64_t D) {
-  const size_t w2 = size_t(sm_count()) * wq::kv8::WARPS * 2, rb = size_t(8 * row_blocks(max_rows, D));
+Ws attn_ws(int64_t B, int64_t D) {
+  const size_t w2 = size_t(sm_count()) * wq::kv8::MAX_WARPS * 2, rb = size_t(wq::kv8::RB);
   Ws s;
   s.ml = up256(w2 * rb * size_t(D) * 4);
   s.prefix = s.ml + up256(w2 * rb * 8);
@@ -733,11 +738,12 @@ Ws attn_ws(int64_t B, int64_t max_rows, int64_t D) {
   return s;
 }
 
-template <typename TQ, int FMT, int D, int NB>
+template <typename TQ, int FMT, int D>
 int launch_decode(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int max_pos, float scale,
                   void* out, uint8_t* ws, cudaStream_t s) {
   using namespace wq::kv8;
-  auto kern = attn_kv8_kernel<TQ, FMT, D, NB>;
+  auto kern = attn_kv8_kernel<TQ, FMT, D>;
+  constexpr int WARPS = Shape<D>::WARPS;
   constexpr size_t smem = size_t(WARPS) * Shape<D>::WARP_BYTES;
   static std::mutex mu;
   static bool done[64] = {};
@@ -757,14 +763,14 @@ int launch_decode(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int m
                 int(a.kv_heads), tshift};
   const Batch bt{a.table, a.cu, a.lens, int(a.B), int(a.width), int(a.rows), int(a.max_new)};
   const Rope rp{a.cos, a.sin, int(a.rot), max_pos, a.interleaved};
-  const Ws w = attn_ws(a.B, a.max_new * G, D);
+  const Ws w = attn_ws(a.B, D);
   const Args ar{ldq, int(heads), G, scale * 1.4426950408889634f, reinterpret_cast<float*>(ws),
                 reinterpret_cast<float*>(ws + w.ml), reinterpret_cast<int64_t*>(ws + w.prefix)};
   const int grid = sm_count();
   TQ* o = static_cast<TQ*>(out);
   kern<<<grid, WARPS * 32, smem, s>>>(static_cast<const TQ*>(Q), o, c, bt, rp, ar, status_ptr());
   WQ_LAUNCH_CHECK("attn_kv8_kernel");
-  const int64_t most_rb = (a.max_new * G + 8 * NB - 1) / (8 * NB);
+  const int64_t most_rb = (a.max_new * G + RB - 1) / RB;
   const int64_t joins = a.B * a.kv_heads * most_rb;
   if (joins > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
@@ -776,7 +782,7 @@ int launch_decode(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int m
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<TQ, FMT, D, NB>, o, c, bt, ar,
+  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<TQ, D>, o, c, bt, ar,
                                    int64_t(grid) * WARPS, int(most_rb)));
   return WQ_OK;
 }
@@ -784,26 +790,17 @@ int launch_decode(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int m
 template <typename TQ, int FMT>
 int launch_by_shape(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int max_pos,
                     float scale, void* out, uint8_t* ws, cudaStream_t s) {
-  const int nb = row_blocks(a.max_new * (heads / a.kv_heads), a.D);
-#define WQ_ATTN(D_, NB_) \
-  return launch_decode<TQ, FMT, D_, NB_>(Q, ldq, heads, a, max_pos, scale, out, ws, s)
-  if (a.D == 64) {
-    if (nb == 1) WQ_ATTN(64, 1);
-    WQ_ATTN(64, 2);
-  }
-  if (a.D == 128) {
-    if (nb == 1) WQ_ATTN(128, 1);
-    WQ_ATTN(128, 2);
-  }
-  WQ_ATTN(256, 1);
-#undef WQ_ATTN
+  if (a.D == 64) return launch_decode<TQ, FMT, 64>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
+  if (a.D == 128) return launch_decode<TQ, FMT, 128>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
+  return launch_decode<TQ, FMT, 256>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
 }
 
 }  // namespace
 
 size_t attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
                                 int64_t max_q) {
-  return attn_ws(B, max_q * (heads / kv_heads), D).bytes;
+  (void)heads, (void)kv_heads, (void)max_q;
+  return attn_ws(B, D).bytes;
 }
 
 int launch_attn_kv8(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
