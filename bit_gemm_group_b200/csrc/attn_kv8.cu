@@ -16,7 +16,9 @@
 // Work is cut into units of TK positions of one (sequence, head, row block),
 // numbered with the position fastest, and every warp of the grid takes an
 // equal run of them, whatever the sequences' lengths: no warp waits for
-// another.  A run's whole segments are written out directly; cut ones go to
+// another.  A segment (all units of a row block) counts one unit more, for its
+// queries and its result: without it the warps that got many short sequences
+// ended a quarter later than the rest.  A run's whole segments are written out directly; cut ones go to
 // the workspace and attn_kv8_join_kernel adds them in a fixed order.
 //
 // Softmax in one pass, in base 2, with the value scale folded into the
@@ -52,8 +54,8 @@ struct Shape {
   static constexpr int KP = D, VP = D == 64 ? 80 : D;
   static constexpr int KBYTES = TK * KP, VBYTES = TK * VP;
   static constexpr int STAGE = KBYTES + VBYTES + 32;  // + scales of up to two pages
-  static constexpr int QP = D + 8;                    // halves per staged query row
-  static constexpr int WARP_BYTES = STAGES * STAGE + 8 * QP * 2;
+  static constexpr int QP = 2 * D + 8;                // halves per staged query row
+  static constexpr int WARP_BYTES = STAGES * STAGE + 4 * QP * 2;
 };
 
 __device__ __forceinline__ int swz(int D, int row, int piece) {
@@ -176,6 +178,7 @@ __device__ __forceinline__ int64_t workers(int64_t U, int64_t W) {
 struct Cursor {
   int b, h, rb, tile;           // sequence, kv head, row block, unit of positions
   int n, q0, len, tiles, nrb;   // of sequence b
+  int at;                       // unit of the run (a segment's first unit is its start)
 
   __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int TK, int* status) {
     n = seq_rows(bt, b, &q0, status);
@@ -189,7 +192,7 @@ struct Cursor {
     tiles = len > 0 ? (len + TK - 1) / TK : 1;
   }
   __device__ __forceinline__ int64_t units(int heads) const {
-    return n > 0 ? int64_t(nrb) * heads * tiles : 0;
+    return n > 0 ? int64_t(nrb) * heads * (tiles + 1) : 0;
   }
 };
 
@@ -280,14 +283,17 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   me.b = start_b[warp];
   me.load(bt, c.tshift, ar.G, TK, nullptr);
   {
-    const int64_t at = start_at[warp];
-    me.tile = int(at % me.tiles);
-    const int64_t seg = at / me.tiles;
+    const int64_t at = start_at[warp], seg = at / (me.tiles + 1);
+    me.at = 0;
+    me.tile = int(at - seg * (me.tiles + 1)) - 1;
+    if (me.tile < 0) me.tile = 0, me.at = 1;  // the run begins with the segment's own unit
     me.rb = int(seg % me.nrb);
     me.h = int(seg / me.nrb);
   }
   auto advance = [&](Cursor& s) {
+    ++s.at;
     if (++s.tile < s.tiles) return;
+    ++s.at;
     s.tile = 0;
     if (++s.rb < s.nrb) return;
     s.rb = 0;
@@ -307,7 +313,8 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
 
   // ------------------------------------------------ the copies, a few units ahead
   Cursor ahead = me;
-  int64_t issued = u0;
+  int issued = 0;
+  const int count = int(u1 - u0);
   int pg0 = -1, pg1 = -1;  // the pages of the unit to be copied next
   auto pages_of = [&](const Cursor& s) {
     const int col = (s.tile * TK) >> c.tshift;
@@ -317,44 +324,52 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   };
   pages_of(ahead);
   auto issue = [&]() {
-    if (issued < u1) {
-      const uint32_t st = base + uint32_t((issued - u0) % S::STAGES) * S::STAGE;
+    if (ahead.at < count) {
+      const uint32_t st = base + uint32_t(issued % S::STAGES) * S::STAGE;
       const int tok0 = ahead.tile * TK, col = tok0 >> c.tshift;
       const bool ok0 = pg0 >= 0 && pg0 < c.pages, ok1 = pg1 >= 0 && pg1 < c.pages;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bool used = (k == 0 || T_ < TK) && ((col + k) << c.tshift) < ahead.len;
-        if (lane == k && (used || k == 0)) {
-          const uint32_t sc = st + S::KBYTES + S::VBYTES + 8 * k;
-          if (k ? ok1 : ok0) {
-            cp4(sc, c.ks + c.block(k ? pg1 : pg0, ahead.h));
-            cp4(sc + 4, c.vs + c.block(k ? pg1 : pg0, ahead.h));
-          } else {
-            // no such page: its positions are masked
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sc), "f"(0.f), "f"(-1.f)
-                         : "memory");
-            if (used) record_error(status, WQ_ERR_ARG);
-          }
+      if (lane < 2 && (lane == 0 || T_ < TK)) {
+        const bool ok = lane ? ok1 : ok0, used = ((col + lane) << c.tshift) < ahead.len;
+        const uint32_t sc = st + S::KBYTES + S::VBYTES + 8 * lane;
+        if (ok) {
+          const int64_t at = c.block(lane ? pg1 : pg0, ahead.h);
+          cp4(sc, c.ks + at);
+          cp4(sc + 4, c.vs + at);
+        } else {
+          // no page: its positions are masked
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sc), "f"(0.f), "f"(-1.f)
+                       : "memory");
+          if (used) record_error(status, WQ_ERR_ARG);
         }
       }
       // rows are contiguous in a page, so a lane's pieces are 512 bytes apart
       constexpr int PER = D / 16, STEP = 32 / PER, COPIES = TK / STEP;
       const int rows = ahead.len - tok0, r0 = lane / PER, piece = lane % PER;
       const int64_t at0 = ((c.block(ok0 ? pg0 : 0, ahead.h) << c.tshift) + (tok0 & (T_ - 1))) * D + lane * 16;
-      const int64_t at1 =
-          T_ < TK ? (c.block(ok1 ? pg1 : 0, ahead.h) << c.tshift) * D + lane * 16 - 16 * D : at0;
+      if (T_ >= TK && ok0 && rows >= TK) {
+        const uint8_t *pk = c.kq + at0, *pv = c.vq + at0;
 #pragma unroll
-      for (int i = 0; i < COPIES; ++i) {
-        const int r = r0 + i * STEP;
-        const bool second = T_ < TK && i >= COPIES / 2;
-        const bool valid = r < rows && (second ? ok1 : ok0);
-        const int64_t at = (second ? at1 : at0) + i * 512;
-        cp16z(st + r * S::KP + swz(D, r, piece) * 16, c.kq + at, valid);
-        cp16z(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, c.vq + at, valid);
+        for (int i = 0; i < COPIES; ++i) {
+          const int r = r0 + i * STEP;
+          cp16(st + r * S::KP + swz(D, r, piece) * 16, pk + i * 512);
+          cp16(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, pv + i * 512);
+        }
+      } else {
+        const int64_t at1 =
+            T_ < TK ? (c.block(ok1 ? pg1 : 0, ahead.h) << c.tshift) * D + lane * 16 - 16 * D : at0;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int r = r0 + i * STEP;
+          const bool second = T_ < TK && i >= COPIES / 2;
+          const bool valid = r < rows && (second ? ok1 : ok0);
+          const int64_t at = (second ? at1 : at0) + i * 512;
+          cp16z(st + r * S::KP + swz(D, r, piece) * 16, c.kq + at, valid);
+          cp16z(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, c.vq + at, valid);
+        }
       }
       ++issued;
       advance(ahead);
-      if (issued < u1) pages_of(ahead);
+      if (ahead.at < count) pages_of(ahead);
     }
     cp_commit();
   };
@@ -368,20 +383,25 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   bool fresh = true, first_seg = true;
   int seg_tile0 = me.tile;
 
-  for (int64_t u = u0; u < u1; ++u) {
+  for (int u = 0; me.at < count; ++u) {
     if (fresh) {
       // -------------------------------------------- a segment's queries
       fresh = false;
       seg_tile0 = me.tile;
-      constexpr int P = D / 8, RPP = 32 / P;
+      // P lanes per row, 32 / P rows at a time; rows are loaded together (all
+      // eight, or four of 256 elements) and staged four at a time
+      constexpr int P = D / 8, RPP = 32 / P, ITER = RB / RPP, HALF = ITER / 2;
+      constexpr int LOADS = ITER > 4 ? HALF : ITER;
+      const int d = (lane % P) * 8;
+      float x[LOADS][8];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {  // rounded to f16, then what that left
-        __syncwarp();
-#pragma unroll 1
-        for (int r0 = 0; r0 < RB; r0 += RPP) {
-          const int r = r0 + lane / P, d = (lane % P) * 8;
-          const int rr = me.rb * RB + r;
-          float x[8] = {};
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          if (half == 1 && LOADS == ITER) break;
+          const int rr = me.rb * RB + (half * HALF + k) * RPP + lane / P;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
           if (rr < me.n * ar.G) {
             const int i = rr / ar.G;
             int pos = me.len - me.n + i;
@@ -393,11 +413,15 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
             }
             const TQ* row = Q + int64_t(me.q0 + i) * ar.ldq +
                             int64_t(me.h * ar.G + (rr - i * ar.G)) * D;
-            rotated8(row, d, pos, rq, x);
+            rotated8(row, d, pos, rq, x[k]);
           }
-          float a = 0.f;
+        }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+        for (int j = 0; j < HALF; ++j) {
+          const int k = LOADS == ITER ? half * HALF + j : j;
+          float a = 0.f, sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[k][e]));
 #pragma unroll
           for (int o = P / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
           // a power of two brings the row's largest element to [2^14, 2^15)
@@ -406,40 +430,46 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
                        : 0;
           ex = ex > 100 ? 100 : ex;
           const float up = __uint_as_float(uint32_t(127 + ex) << 23);
-          float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] *= up;
-            sum += x[e];
-            if (part) x[e] -= __half2float(__float2half_rn(x[e]));
+            x[k][e] *= up;
+            sum += x[k][e];
           }
-          uint4 o;
-          o.x = f16x2(x[0], x[1]);
-          o.y = f16x2(x[2], x[3]);
-          o.z = f16x2(x[4], x[5]);
-          o.w = f16x2(x[6], x[7]);
-          *reinterpret_cast<uint4*>(qs + r * S::QP + d) = o;
-          if (part == 0) {
 #pragma unroll
-            for (int q = P / 2; q > 0; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
-            if (lane % P == 0)
-              *reinterpret_cast<float2*>(qs + r * S::QP + D) =
-                  make_float2(__uint_as_float(uint32_t(127 - ex) << 23), sum);
+          for (int o = P / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          // rounded to f16, and what that left: word e of both side by side
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(x[k][2 * e], x[k][2 * e + 1]);
+            const float2 f = __half22float2(h);
+            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+            lo[e] = f16x2(x[k][2 * e] - f.x, x[k][2 * e + 1] - f.y);
           }
+          __half* dst = qs + (j * RPP + lane / P) * S::QP;
+          *reinterpret_cast<uint4*>(dst + 2 * d) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          *reinterpret_cast<uint4*>(dst + 2 * d + 8) = make_uint4(hi[2], hi[3], lo[2], lo[3]);
+          if (lane % P == 0)
+            *reinterpret_cast<float2*>(dst + 2 * D) =
+                make_float2(__uint_as_float(uint32_t(127 - ex) << 23), sum);
         }
         __syncwarp();
+        if (g >> 2 == half) {
+          const uint32_t row = qbase + uint32_t((g & 3) * S::QP) * 2;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int j = ks >> 2, w = ks & 3;
-          const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
-          const uint2 v = lds64(qbase + uint32_t(g * S::QP + pc * 16 + w * 4) * 2);
-          qa[ks][part] = v.x;
-          qa[ks][2 + part] = v.y;
+          for (int ks = 0; ks < KS; ++ks) {
+            const int j = ks >> 2, w = ks & 3;
+            const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
+            const uint4 v = lds128(row + uint32_t(2 * (pc * 16 + w * 4)) * 2);
+            qa[ks][0] = v.x;
+            qa[ks][1] = v.z;
+            qa[ks][2] = v.y;
+            qa[ks][3] = v.w;
+          }
+          fq = lds32f(row + 4 * D) * ar.scale_log2 * Code<FMT>::KEY;
+          start = -Code<FMT>::BIAS * lds32f(row + 4 * D + 4);
         }
-        if (part == 0) {
-          fq = lds32f(qbase + uint32_t(g * S::QP + D) * 2) * ar.scale_log2 * Code<FMT>::KEY;
-          start = -Code<FMT>::BIAS * lds32f(qbase + uint32_t(g * S::QP + D) * 2 + 4);
-        }
+        __syncwarp();
       }
       const int rr = me.rb * RB + g;
       lim = rr < me.n * ar.G ? min(me.len, me.len - me.n + rr / ar.G + 1) : 0;
@@ -453,7 +483,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     cp_wait<S::STAGES - 2>();
     __syncwarp();
     issue();
-    const uint32_t st = base + uint32_t((u - u0) % S::STAGES) * S::STAGE;
+    const uint32_t st = base + uint32_t(u % S::STAGES) * S::STAGE;
     const uint32_t vb = st + S::KBYTES, scb = vb + S::VBYTES;
 
     // -------------------------------------------------- scores
@@ -482,29 +512,36 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     }
 
     // -------------------------------------------------- softmax, base 2
-    float k0 = lds32f(scb), v0 = lds32f(scb + 4), k1 = k0, v1 = v0;
-    if (T_ < TK) {
-      k1 = lds32f(scb + 8);
-      v1 = lds32f(scb + 12);
-      if (((((me.tile * TK) >> c.tshift) + 1) << c.tshift) >= me.len) k1 = 0.f, v1 = -1.f;
-    }
-    const float lv0 = v0 < 0.f ? -CUDART_INF_F : __log2f(fmaxf(v0, 1e-30f));
-    const float lv1 = v1 < 0.f ? -CUDART_INF_F : __log2f(fmaxf(v1, 1e-30f));
-    const float rv0 = __fdividef(1.f, fmaxf(v0, 1e-30f)), rv1 = __fdividef(1.f, fmaxf(v1, 1e-30f));
-    const float f0 = fq * k0, f1 = fq * k1;
+    // (the unit's second page, where it has two, is that of the upper half)
+    auto page_scales = [&](int k, float& f, float& lv, float& rv) {
+      const float ks = lds32f(scb + 8 * k), vs = lds32f(scb + 8 * k + 4);
+      const float v = fmaxf(vs, 1e-30f);
+      f = fq * ks;
+      lv = vs < 0.f ? -CUDART_INF_F : __log2f(v);
+      rv = __fdividef(1.f, v);
+    };
+    float f0, lv0, rv0, f1, lv1, rv1;
+    page_scales(0, f0, lv0, rv0);
+    f1 = f0, lv1 = lv0, rv1 = rv0;
+    if (T_ < TK) page_scales(1, f1, lv1, rv1);
     float mx = -CUDART_INF_F;
-    const bool edge = __any_sync(0xffffffffu, (me.tile + 1) * TK > lim);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool hi = NT == 4 && nt >= 2;  // the unit's second page, where it has two
+      const bool hi = NT == 4 && nt >= 2;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float& x = sc[nt][e];
-        x = fmaf(x + sc[nt][2 + e], hi ? f1 : f0, hi ? lv1 : lv0);
-        if (edge && me.tile * TK + nt * 8 + 2 * t + e >= lim) x = -CUDART_INF_F;
-        mx = fmaxf(mx, x);
-      }
+      for (int e = 0; e < 2; ++e)
+        sc[nt][e] = fmaf(sc[nt][e] + sc[nt][2 + e], hi ? f1 : f0, hi ? lv1 : lv0);
     }
+    if (__any_sync(0xffffffffu, (me.tile + 1) * TK > lim)) {
+      const int left = lim - me.tile * TK - 2 * t;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (nt * 8 + e >= left) sc[nt][e] = -CUDART_INF_F;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][0], sc[nt][1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (__any_sync(0xffffffffu, mx > m + LAG)) {
@@ -568,7 +605,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     }
 
     // -------------------------------------------------- end of a segment
-    const bool last = me.tile + 1 == me.tiles || u + 1 == u1;
+    const bool last = me.tile + 1 == me.tiles || me.at + 1 >= count;
     if (last) {
       const bool whole = seg_tile0 == 0 && me.tile + 1 == me.tiles;
       const int64_t part = id * 2 + (first_seg ? 0 : 1);
@@ -643,7 +680,7 @@ __global__ void __launch_bounds__(1024)
   s.load(bt, c.tshift, ar.G, Shape<D>::TK, nullptr);
   if (s.n == 0 || rb >= s.nrb) return;
   const int64_t U = ar.prefix[bt.B], W = workers(U, total_warps);
-  const int64_t f = ar.prefix[b] + (int64_t(h) * s.nrb + rb) * s.tiles;
+  const int64_t f = ar.prefix[b] + (int64_t(h) * s.nrb + rb) * (s.tiles + 1) + 1;
   const int64_t wa = run_owner(f, U, W), wb = run_owner(f + s.tiles - 1, U, W);
   if (wa == wb) return;
 
@@ -660,7 +697,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int e = 0; e < PER; ++e) po[k][e] = 0.f;
       if (w <= wb) {
-        const int64_t row = (w * 2 + (run_start(w, U, W) >= f ? 0 : 1)) * RB + r;
+        const int64_t row = (w * 2 + (run_start(w, U, W) >= f - 1 ? 0 : 1)) * RB + r;
         pm[k] = __ldcg(ar.part_ml + row * 2);
         pl[k] = __ldcg(ar.part_ml + row * 2 + 1);
 #pragma unroll
