@@ -39,8 +39,6 @@ namespace kv8 {
 
 constexpr int MAX_WARPS = 12;
 constexpr int RB = 8;      // rows per block
-constexpr float LAG = 8.f;  // how far the maximum may grow before the sums are rescaled
-constexpr float OFF = 6.f;
 
 template <int D_>
 struct Shape {
@@ -97,12 +95,6 @@ __device__ __forceinline__ float lds32f(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Codes as f16 pairs, exactly.
 // Keys: int8 as u = c + 128 in the subnormals (u 2^-24); the score of -128
 //   ones is where a row's sum starts.  E4M3 through the hardware conversion.
@@ -157,23 +149,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t f16x2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Units [u0, u1) of worker w: [w U / W, (w + 1) U / W).
-__device__ __forceinline__ int64_t run_start(int64_t w, int64_t U, int64_t W) { return w * U / W; }
-__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t U, int64_t W) {
-  return ((u + 1) * W - 1) / U;
-}
-// Workers in use: no run is shorter than two units (a cut run costs a part in
-// the workspace, about a unit's bytes).
-__device__ __forceinline__ int64_t workers(int64_t U, int64_t W) {
-  const int64_t w = (U + 1) / 2;
-  return w < W ? w : W;
-}
-
 // A sequence as this kernel sees it, and a position in the numbering of units.
 struct Cursor {
   int b, h, rb, tile;           // sequence, kv head, row block, unit of positions
@@ -836,12 +811,15 @@ int launch_by_shape(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int
 
 size_t attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
                                 int64_t max_q) {
-  (void)heads, (void)kv_heads, (void)max_q;
+  if (attn_kv8_on_tc(heads, kv_heads, D, max_q))
+    return attn_kv8_tc_workspace_bytes(B, heads, kv_heads, D, max_q);
   return attn_ws(B, D).bytes;
 }
 
 int launch_attn_kv8(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
                     int max_pos, float scale, void* out, void* ws, cudaStream_t s) {
+  if (attn_kv8_on_tc(heads, a.kv_heads, a.D, a.max_new))
+    return launch_attn_kv8_tc(Q, dtype, ldq, heads, a, max_pos, scale, out, ws, s);
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool i8 = a.fmt == WQ_W8_INT8;
   if (dtype == WQ_BF16)

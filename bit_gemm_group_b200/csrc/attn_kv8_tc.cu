@@ -1,0 +1,850 @@
+// attn_kv8_tc.cu -- causal attention over the paged 8-bit cache for more than 8
+// rows to a (sequence, kv head): prompts, chunks of prompts, drafts.
+//
+// The mathematics of attn_kv8.cu on the fifth-generation tensor cores.  One CTA
+// per SM of 13 warps; 128 rows (query, head) are one tensor-core tile:
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a row per thread: scores
+//                   from tensor memory, weights back to it as f16
+//   warps 8-11      converters: 128 positions of codes at a time from the pages
+//                   to f16 (exactly) in shared memory, keys and values in the
+//                   same 128-byte swizzled layout (values are the product's
+//                   K operand along their rows: MN-major)
+//   warp 12         issues tcgen05.mma kind::f16: scores Q K^T (both operands
+//                   in shared memory), then weights (tensor memory) times V
+//
+// PAIR: the two tiles are 256 rows of one (sequence, head) and share every
+// converted block, which halves the conversion work: prompts.  Otherwise both
+// tiles are the same 128 rows and take the blocks in turn, each with sums of its
+// own that are joined at the end: drafts (while one tile's softmax runs the
+// tensor cores work for the other), and fp16 inputs, whose queries are two f16
+// terms (rounded, and what that left) so that a result is good to fp16.
+//
+// Bound by the tensor cores and the exponentials together: a 128 x 128 block of
+// scores is 2 x 512 cycles of MMA and 1024 of the special-function units at
+// D = 128.  With few rows it is bound by the blocks' latency.
+//
+// Items (row tile, head) are cut into blocks of 128 positions and numbered; each
+// CTA takes an equal run of blocks, with START more for each item, and joins
+// cut items as attn_kv8.cu does.
+#include <math_constants.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace wq {
+namespace kv8 {
+namespace tcore {
+
+constexpr int THREADS = 13 * 32;
+constexpr int TK = 128;    // positions per block
+constexpr int START = 2;   // units an item's queries and results count
+
+template <int D>
+struct Smem {
+  static constexpr int TILE = 128 * D * 2;  // 128 rows of f16
+  static constexpr int BLOCKS = 6 * TILE;   // Q 2, K 2, V 2
+  struct Ctrl {
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], qfull;
+    uint64_t sfull[2], pfull[2], odone[2], scfull[4], mfull, mfree, drain;
+    float4 scale[4][8];     // per block in flight and 16 positions: ks, log2 vs, 1 / vs
+    float m[128], l[128];   // of tile 1, where both tiles are the same rows
+    int64_t sum[13], start_off;
+    int start_p, tmem_base, abort_flag;
+  };
+  static constexpr size_t BYTES = 1024 + BLOCKS + sizeof(Ctrl);
+};
+
+constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (8u << 24);
+}
+// MN-major operand in 128-byte swizzled rows of 64 elements: groups of 64
+// elements `lbo` bytes apart, groups of 8 rows (positions) 1024.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= uint64_t((addr & 0x3FFFFu) >> 4);
+  d |= uint64_t(lbo >> 4) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
+// Four codes of a word as two f16 pairs (see attn_kv8.cu).
+template <int FMT>
+__device__ __forceinline__ void expand(uint32_t w, uint32_t& a, uint32_t& b) {
+  if (FMT == WQ_W8_INT8) {
+    const uint32_t x = w ^ 0x80808080u;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(x, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(x, 0x64646464u, 0x4342)), "r"(0x64806480u));
+  } else {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+struct TcArgs {
+  int64_t ldq;
+  int heads, G, most_r;  // query heads, heads per kv head, row tiles of the longest sequence
+  float scale_log2;
+  float* parts;     // [2 W][ROWS][D]
+  float* part_ml;   // [2 W][ROWS][2]
+  int64_t* prefix;  // [B most_r + 1] first unit of each (sequence, row tile)
+};
+
+// An item's (sequence, row tile) and how many blocks it has.
+struct Item {
+  int b, r, h;
+  int n, q0, len, R, tiles;
+  __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int rows, int* status) {
+    n = seq_rows(bt, b, &q0, status);
+    len = __ldg(bt.lens + b);
+    const int64_t most = int64_t(bt.width) << tshift;
+    if (len < 0 || len > most) {
+      record_error(status, WQ_ERR_ARG);
+      len = len < 0 ? 0 : int(most);
+    }
+    R = int((int64_t(n) * G + rows - 1) / rows);
+    row_tile(G, rows);
+  }
+  __device__ __forceinline__ void row_tile(int G, int rows) {
+    int64_t i = (int64_t(r + 1) * rows - 1) / G;  // the tile's last query
+    if (i > n - 1) i = n - 1;
+    int seen = len - n + int(i) + 1;
+    seen = seen > len ? len : seen;
+    tiles = seen > 0 ? (seen + TK - 1) / TK : 1;
+  }
+  __device__ __forceinline__ bool valid() const { return n > 0 && r < R; }
+};
+
+// Walks over the work of a CTA's run: the item and its blocks [t0, t1).
+struct Walk {
+  Item it;
+  int64_t begin, u0, u1;  // first unit of the item; the run
+  int t0, t1;
+  bool first;
+  __device__ __forceinline__ void clip() {
+    const int64_t a = u0 - begin - START, e = u1 - begin - START;
+    t0 = a > 0 ? int(a) : 0;
+    t1 = e < it.tiles ? int(e) : it.tiles;
+  }
+  // the next item with blocks in the run; false at its end
+  __device__ __forceinline__ bool next(const Batch& bt, int heads, int tshift, int G, int rows) {
+    while (true) {
+      begin += it.tiles + START;
+      if (begin >= u1) return false;
+      if (++it.h == heads) {
+        it.h = 0;
+        if (++it.r < it.R) {
+          it.row_tile(G, rows);
+        } else {
+          it.r = 0;
+          do {
+            if (++it.b >= bt.B) return false;
+            it.load(bt, tshift, G, rows, nullptr);
+          } while (it.n == 0);
+        }
+      }
+      clip();
+      if (t1 > t0) return true;
+    }
+  }
+};
+
+template <typename TQ, int FMT, int D, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_kv8_tc_kernel(const TQ* __restrict__ Q, TQ* __restrict__ O, Cache c, Batch bt, Rope rp,
+                       TcArgs ar, int* status, uint64_t limit_ns) {
+  using S = Smem<D>;
+  constexpr int ROWS = PAIR ? 256 : 128;
+  constexpr bool TWO = !PAIR && std::is_same<TQ, __half>::value;  // queries in two terms
+  constexpr int PLANE = 128 * 128;  // 128 rows of 64 f16
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  auto& sm = *reinterpret_cast<typename S::Ctrl*>(base + S::BLOCKS);
+  const uint32_t qs = tc::smem_u32(base), ksm = qs + 2 * S::TILE, vsm = ksm + 2 * S::TILE;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T_ = 1 << c.tshift;
+
+  // ------------------------------------------------ the run of this CTA
+  const int P = bt.B * ar.most_r;
+  int64_t U = 0, u0 = 0, u1 = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t run = 0;
+    for (int p0 = 0; p0 < P; p0 += THREADS) {
+      const int p = p0 + int(threadIdx.x);
+      int64_t mine = 0;
+      if (p < P) {
+        Item it;
+        it.b = p / ar.most_r;
+        it.r = p - it.b * ar.most_r;
+        it.load(bt, c.tshift, ar.G, ROWS, pass ? nullptr : status);
+        if (it.valid()) mine = int64_t(it.tiles + START) * c.heads;
+      }
+      int64_t inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) sm.sum[warp] = inc;
+      __syncthreads();
+      int64_t before = run;
+      for (int w = 0; w < warp; ++w) before += sm.sum[w];
+      for (int w = 0; w < 13; ++w) run += sm.sum[w];
+      const int64_t first = before + inc - mine;
+      if (pass == 1) {
+        if (mine > 0 && u0 >= first && u0 < first + mine) {
+          sm.start_p = p;
+          sm.start_off = u0 - first;
+        }
+        if (blockIdx.x == 0 && p < P) {
+          ar.prefix[p] = first;
+          if (p == P - 1) ar.prefix[P] = U;
+        }
+      }
+      __syncthreads();
+    }
+    if (pass == 0) {
+      U = run;
+      const int64_t W = workers(U, gridDim.x);
+      u0 = U && blockIdx.x < W ? run_start(blockIdx.x, U, W) : -1;
+      u1 = U && blockIdx.x < W ? run_start(blockIdx.x + 1, U, W) : -1;
+      if (U == 0) return;
+    }
+  }
+  if (u0 < 0) return;
+  Walk wk;
+  wk.u0 = u0, wk.u1 = u1;
+  wk.it.b = sm.start_p / ar.most_r;
+  wk.it.r = sm.start_p - wk.it.b * ar.most_r;
+  wk.it.load(bt, c.tshift, ar.G, ROWS, nullptr);
+  wk.it.h = int(sm.start_off / (wk.it.tiles + START));
+  wk.begin = u0 - (sm.start_off - int64_t(wk.it.h) * (wk.it.tiles + START));
+  wk.clip();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.kfull[i], 4);
+      tc::mbar_init(&sm.vfull[i], 4);
+      tc::mbar_init(&sm.kempty[i], 1);
+      tc::mbar_init(&sm.vempty[i], 1);
+      tc::mbar_init(&sm.sfull[i], 1);
+      tc::mbar_init(&sm.pfull[i], 4);
+      tc::mbar_init(&sm.odone[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.scfull[i], 1);
+    tc::mbar_init(&sm.mfull, 4);
+    tc::mbar_init(&sm.mfree, 4);
+    tc::mbar_init(&sm.qfull, 8);
+    tc::mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(reinterpret_cast<uint32_t*>(&sm.tmem_base), 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = uint32_t(sm.tmem_base);
+  const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
+  bool more = wk.t1 > wk.t0 || wk.next(bt, c.heads, c.tshift, ar.G, ROWS);
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int x = warp >> 2;                       // tile
+    const int row = (warp & 3) * 32 + lane;        // of the tile
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t st = tmem + lanes + uint32_t(x) * 128;        // scores, weights
+    const uint32_t ot = tmem + lanes + 256 + uint32_t(x) * 128;  // result
+    uint32_t op = 0;  // tensor-core rounds of this tile so far
+    bool ok = true, first_seg = true;
+    uint32_t block = 0, seg = 0;  // blocks and items of the CTA so far
+    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
+      const Item& it = wk.it;
+      const int rr = it.r * ROWS + (PAIR ? x * 128 : 0) + row;
+      const bool live = rr < it.n * ar.G;
+      const int i = live ? rr / ar.G : 0;
+      const int pos = it.len - it.n + i;
+      const int lim = live ? min(it.len, pos + 1) : 0;
+      // -------- this row of queries, as f16 in the swizzled operand layout
+      float fq;
+      {
+        const TQ* src = Q + int64_t(it.q0 + i) * ar.ldq + int64_t(it.h * ar.G + (rr - i * ar.G)) * D;
+        Rope rq = rp;
+        if (pos < 0 || (rq.cos != nullptr && pos >= rq.max_pos)) {
+          if (pos >= 0 && live) record_error(status, WQ_ERR_ARG);
+          rq.cos = nullptr;
+        }
+        float a = 0.f;
+        if (live)
+#pragma unroll 4
+          for (int d = 0; d < D; d += 8) {
+            float v[8];
+            rotated8(src, d, pos, rq, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+          }
+        // a power of two brings the row's largest element to [2^14, 2^15)
+        int ex = (a > 0.f && a <= 3.4028234663852886e38f) ? 141 - int(__float_as_uint(a) >> 23) : 0;
+        ex = ex > 100 ? 100 : ex;
+        const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+        fq = __uint_as_float(uint32_t(127 - ex) << 23) * ar.scale_log2;
+        // one term: with shared rows each group of warps writes half of it;
+        // two terms: group 0 the rounded query, group 1 what that left
+        const int d0 = !PAIR && !TWO ? x * (D / 2) : 0, d1 = !PAIR && !TWO ? d0 + D / 2 : D;
+        const uint32_t dst = qs + ((PAIR || TWO) ? x * S::TILE : 0) + row * 128;
+#pragma unroll 2
+        for (int d = d0; d < d1; d += 8) {
+          float v[8] = {};
+          if (live) rotated8(src, d, pos, rq, v);
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = v[2 * e] * up, q = v[2 * e + 1] * up;
+            if (TWO && x == 1) {
+              p -= __half2float(__float2half_rn(p));
+              q -= __half2float(__float2half_rn(q));
+            }
+            h[e] = f16x2(p, q);
+          }
+          sts128(dst + (d / 64) * PLANE + ((((d & 63) >> 3) ^ (row & 7)) << 4), h[0], h[1], h[2],
+                 h[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.qfull);
+      }
+
+      float m = -CUDART_INF_F, l = 0.f;
+      const int J = wk.t1 - wk.t0;
+      int done = 0;  // of this tile in this segment
+      for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
+        const uint32_t b = block + uint32_t(j);
+        if (!(ok = tc::wait_warp(&sm.sfull[x], op & 1u, wd) &&
+                   tc::wait_warp(&sm.scfull[b & 3], (b >> 2) & 1u, wd)))
+          break;
+        tc::fence_after_sync();
+        const int tok0 = (wk.t0 + j) * TK;
+        const float4* scl = sm.scale[b & 3];
+        // -------- the row's maximum
+        const bool edge = __any_sync(0xffffffffu, tok0 + TK > lim);
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          tc::tmem_ld_x32(st + q * 32, s);
+          tc::tmem_wait_ld();
+          if (edge)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (tok0 + q * 32 + e >= lim) s[e] = 0xFF800000u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float4 f = scl[2 * q + k];
+            float a = __uint_as_float(s[16 * k]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) a = fmaxf(a, __uint_as_float(s[16 * k + e]));
+            mx = fmaxf(mx, a == -CUDART_INF_F ? a : fmaf(a, fq * f.x, f.y));
+          }
+        }
+        if (__any_sync(0xffffffffu, mx > m + LAG)) {
+          const float now = fmaxf(m, mx);
+          const float al = now == m ? 1.f : exp2_approx(m - now);
+          m = now;
+          l *= al;
+          if (done) {
+            // the products that add to the result so far are complete
+            if (!(ok = tc::wait_warp(&sm.odone[x], (op - 1) & 1u, wd))) break;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tc::tmem_ld_x16(ot + q * 16, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tc::tmem_st_x16(ot + q * 16, o);
+            }
+          }
+        }
+        // -------- weights
+        const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          tc::tmem_ld_x32(st + q * 32, s);
+          tc::tmem_wait_ld();
+          if (edge)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (tok0 + q * 32 + e >= lim) s[e] = 0xFF800000u;
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float4 f = scl[2 * q + k];
+            const float mul = fq * f.x, add = f.y + off;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float a = exp2_approx(fmaf(__uint_as_float(s[16 * k + 2 * e]), mul, add));
+              const float b = exp2_approx(fmaf(__uint_as_float(s[16 * k + 2 * e + 1]), mul, add));
+              sum += a + b;
+              p[8 * k + e] = f16x2(a, b);
+            }
+            l = fmaf(sum, f.z, l);
+          }
+          tc::tmem_st_x16(st + q * 16, p);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.pfull[x]);
+      }
+      if (!ok) break;
+      if (done) {
+        if (!(ok = tc::wait_warp(&sm.odone[x], (op - 1) & 1u, wd))) break;
+        tc::fence_after_sync();
+      }
+      // -------- results
+      const bool whole = wk.t0 == 0 && wk.t1 == it.tiles;
+      const int64_t part = int64_t(blockIdx.x) * 2 + (first_seg ? 0 : 1);
+      float w0 = 1.f, w1 = 0.f;
+      bool both = false;
+      if (!PAIR) {
+        // tile 1's sums join tile 0's
+        if (x == 1) {
+          sm.m[row] = m, sm.l[row] = l;
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.mfull);
+        } else {
+          if (!(ok = tc::wait_warp(&sm.mfull, seg & 1u, wd))) break;
+          tc::fence_after_sync();
+          const float m1 = sm.m[row], l1 = sm.l[row], now = fmaxf(m, m1);
+          both = J > 1;
+          if (now != -CUDART_INF_F) {
+            w0 = exp2_approx(m - now);
+            w1 = exp2_approx(m1 - now);
+            l = l * w0 + l1 * w1;
+            m = now;
+          }
+        }
+      }
+      if (PAIR || x == 0) {
+        const int prow = (PAIR ? x * 128 : 0) + row;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + it.h * ar.G + (rr - i * ar.G)) * D;
+        float* pd = ar.parts + (part * ROWS + prow) * D;
+        if (!whole) {
+          __stcg(ar.part_ml + (part * ROWS + prow) * 2, m);
+          __stcg(ar.part_ml + (part * ROWS + prow) * 2 + 1, l);
+        }
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t a[16], b[16];
+          tc::tmem_ld_x16(ot + q * 16, a);
+          if (both) tc::tmem_ld_x16(ot + 128 + q * 16, b);
+          tc::tmem_wait_ld();
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            v[e] = __uint_as_float(a[e]) * w0;
+            if (both) v[e] = fmaf(__uint_as_float(b[e]), w1, v[e]);
+          }
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              __stcg(reinterpret_cast<float4*>(pd + q * 16 + e),
+                     make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+          } else if (live) {
+#pragma unroll
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+              union {
+                uint4 u;
+                TQ e[8];
+              } y;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if constexpr (std::is_same<TQ, __half>::value)
+                  y.e[e] = __float2half_rn(v[e0 + e] * inv);
+                else
+                  y.e[e] = __float2bfloat16_rn(v[e0 + e] * inv);
+              }
+              *reinterpret_cast<uint4*>(dst + q * 16 + e0) = y.u;
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      if (!PAIR) {
+        // tile 1's result, m and l have been read
+        __syncwarp();
+        if (x == 1)
+          ok = tc::wait_warp(&sm.mfree, seg & 1u, wd);
+        else if (lane == 0)
+          tc::mbar_arrive(&sm.mfree);
+        tc::fence_after_sync();
+      }
+      first_seg = false;
+      block += J;
+    }
+    if (!ok) sm.abort_flag = 1;
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- converters
+    // a thread's pieces: 16 codes of rows tr, tr + STEP, ... of the block
+    constexpr int PER = D / 16, STEP = 128 / PER, N = 128 / STEP;  // N pieces of K and of V
+    const int ct = int(threadIdx.x) - 256, piece = ct % PER, tr = ct / PER;
+    // a piece is two 16-byte parts of a row of 64 f16; lanes of the upper
+    // half planes store them in the other order (bank conflicts)
+    const int plane = piece / 4, part0 = (piece & 3) * 2, swap = plane & 1;
+    uint32_t block = 0;
+    bool ok = true;
+    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS)) {
+      const Item& it = wk.it;
+      const int J = wk.t1 - wk.t0;
+      // page of each 16 positions of a block: lane g of a warp looks up group
+      // g, and in the first warp its scales
+      int page;
+      float ks, vs;
+      auto look_up = [&](int j) {
+        const int tok = (wk.t0 + j) * TK + lane * 16;
+        page = -1, ks = 1.f, vs = -1.f;
+        if (lane < 8 && j < J && tok < it.len) {
+          page = __ldg(bt.table + int64_t(it.b) * bt.width + (tok >> c.tshift));
+          if (page < 0 || page >= c.pages) {
+            record_error(status, WQ_ERR_ARG);
+            page = -1;
+          } else if (warp == 8) {
+            ks = fmaxf(__ldg(c.ks + c.block(page, it.h)), 1e-30f);
+            vs = fmaxf(__ldg(c.vs + c.block(page, it.h)), 1e-30f);
+          }
+        }
+      };
+      auto load = [&](uint4 (&w)[N], const uint8_t* src, int j, int pages) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = tr + i * STEP, tok = (wk.t0 + j) * TK + r;
+          const int pg = __shfl_sync(0xffffffffu, pages, r >> 4);
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (pg >= 0 && tok < it.len)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(
+                src + ((c.block(pg, it.h) << c.tshift) + (tok & (T_ - 1))) * D + piece * 16));
+        }
+      };
+      auto store = [&](const uint4 (&w)[N], uint32_t dst) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = tr + i * STEP;
+          uint32_t h[8];
+          expand<FMT>(w[i].x, h[0], h[1]);
+          expand<FMT>(w[i].y, h[2], h[3]);
+          expand<FMT>(w[i].z, h[4], h[5]);
+          expand<FMT>(w[i].w, h[6], h[7]);
+          const uint32_t p0 = dst + plane * PLANE + r * 128 + ((part0 ^ (r & 7)) << 4);
+          const uint32_t p1 = p0 ^ 16;
+          if (swap) {
+            sts128(p1, h[4], h[5], h[6], h[7]);
+            sts128(p0, h[0], h[1], h[2], h[3]);
+          } else {
+            sts128(p0, h[0], h[1], h[2], h[3]);
+            sts128(p1, h[4], h[5], h[6], h[7]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      uint4 kw[N], vw[N];
+      look_up(0);
+      load(kw, c.kq, 0, page);
+      for (int j = 0; j < J; ++j, ++block) {
+        const uint32_t s = block & 1u, turn = ((block >> 1) & 1u) ^ 1u;
+        // one operand's codes are on their way while the other's are expanded
+        load(vw, c.vq, j, page);
+        const float4 scales =
+            make_float4(ks, vs < 0.f ? -CUDART_INF_F : __log2f(vs), vs < 0.f ? 0.f : __fdividef(1.f, vs), 0.f);
+        look_up(j + 1);
+        ok = tc::wait_warp(&sm.kempty[s], turn, wd);
+        if (!ok) break;
+        if (warp == 8) {
+          if (lane < 8) sm.scale[block & 3][lane] = scales;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.scfull[block & 3]);
+        }
+        store(kw, ksm + s * S::TILE);
+        if (lane == 0) tc::mbar_arrive(&sm.kfull[s]);
+        if (j + 1 < J) load(kw, c.kq, j + 1, page);
+        ok = tc::wait_warp(&sm.vempty[s], turn, wd);
+        if (!ok) break;
+        store(vw, vsm + s * S::TILE);
+        if (lane == 0) tc::mbar_arrive(&sm.vfull[s]);
+      }
+    }
+    if (!ok) sm.abort_flag = 1;
+  } else {
+    // ------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
+      uint32_t block = 0, seg = 0, opx[2] = {0, 0};
+      bool ok = true;
+      for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
+        const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
+        ok = tc::wait_bounded(&sm.qfull, seg & 1u, wd);
+        tc::fence_after_sync();
+        // scores of round k: tile k & 1, block k / 2 (PAIR) or k
+        auto scores = [&](int k) {
+          const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
+          if (!tc::wait_bounded(&sm.kfull[s], (b >> 1) & 1u, wd)) return false;
+          tc::fence_after_sync();
+          const uint32_t kb = ksm + s * S::TILE, qb = qs + (PAIR ? x * S::TILE : 0);
+#pragma unroll
+          for (int term = 0; term < (TWO ? 2 : 1); ++term)
+#pragma unroll
+            for (int k16 = 0; k16 < D / 16; ++k16) {
+              const uint32_t at = (k16 / 4) * PLANE + (k16 & 3) * 32;
+              tc::mma_f16_ss(tmem + x * 128, tc::sdesc_k_sw128(qb + term * S::TILE + at),
+                             tc::sdesc_k_sw128(kb + at), idesc_s, (term | k16) != 0);
+            }
+          tc::mma_commit(&sm.sfull[x]);
+          if (!PAIR || x == 1) tc::mma_commit(&sm.kempty[s]);
+          return true;
+        };
+        for (int k = 0; k < 2 && k < N && ok; ++k) ok = scores(k);
+        for (int k = 0; k < N && ok; ++k) {
+          const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
+          if (!(ok = tc::wait_bounded(&sm.vfull[s], (b >> 1) & 1u, wd))) break;
+          if (!(ok = tc::wait_bounded(&sm.pfull[x], opx[x] & 1u, wd))) break;
+          ++opx[x];
+          tc::fence_after_sync();
+          const uint32_t vb = vsm + s * S::TILE;
+#pragma unroll
+          for (int k16 = 0; k16 < TK / 16; ++k16)
+            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + k16 * 8,
+                           sdesc_mn_sw128(vb + k16 * 2048, PLANE), idesc_o, k > 1 || k16 != 0);
+          tc::mma_commit(&sm.odone[x]);
+          if (!PAIR || x == 1) tc::mma_commit(&sm.vempty[s]);
+          if (k + 2 < N) ok = scores(k + 2);
+        }
+        block += J;
+      }
+      if (!ok) sm.abort_flag = 1;
+      tc::mma_commit(&sm.drain);
+      tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 12) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of cut items: a warp per row, parts in order.
+template <typename TQ, int D, bool PAIR>
+__global__ void __launch_bounds__(256)
+    attn_kv8_tc_join_kernel(TQ* __restrict__ O, Cache c, Batch bt, TcArgs ar, int64_t workers_max) {
+  constexpr int ROWS = PAIR ? 256 : 128, PER = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  // the item that the boundary in front of run w cuts, if no earlier one does
+  const int64_t w = 1 + blockIdx.x / (ROWS / 8);
+  const int P = bt.B * ar.most_r, oct = int(blockIdx.x % (ROWS / 8));
+  const int64_t U = ar.prefix[P], W = workers(U, workers_max);
+  if (w >= W) return;
+  const int64_t u = run_start(w, U, W);
+  int p = 0;
+  for (int hi = P; hi - p > 1;) {  // the last p with prefix[p] <= u
+    const int mid = (p + hi) / 2;
+    if (ar.prefix[mid] <= u)
+      p = mid;
+    else
+      hi = mid;
+  }
+  Item it;
+  it.b = p / ar.most_r;
+  it.r = p - it.b * ar.most_r;
+  it.load(bt, c.tshift, ar.G, ROWS, nullptr);
+  const int h = int((u - ar.prefix[p]) / (it.tiles + START));
+  const int row = oct * 8 + (threadIdx.x >> 5), rr = it.r * ROWS + row;
+  if (rr >= it.n * ar.G) return;
+  const int64_t begin = ar.prefix[p] + int64_t(h) * (it.tiles + START), f = begin + START;
+  const int64_t wa = run_owner(f, U, W), wb = run_owner(f + it.tiles - 1, U, W);
+  if (wa != w - 1 || wa == wb) return;
+  float m = -CUDART_INF_F, l = 0.f, o[PER] = {};
+  for (int64_t w0 = wa; w0 <= wb; w0 += 4) {
+    float pm[4], pl[4], po[4][PER];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t w = w0 + k;
+      pm[k] = -CUDART_INF_F, pl[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) po[k][e] = 0.f;
+      if (w <= wb) {
+        const int64_t at = (w * 2 + (run_start(w, U, W) >= begin ? 0 : 1)) * ROWS + row;
+        pm[k] = __ldcg(ar.part_ml + at * 2);
+        pl[k] = __ldcg(ar.part_ml + at * 2 + 1);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) po[k][e] = __ldcg(ar.parts + at * D + e * 32 + lane);
+      }
+    }
+    float now = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) now = fmaxf(now, pm[k]);
+    if (now == -CUDART_INF_F) now = 0.f;
+    const float a = exp2_approx(m - now);
+    m = now;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] *= a;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = exp2_approx(pm[k] - now);
+      l = fmaf(pl[k], x, l);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(po[k][e], x, o[e]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int i = rr / ar.G;
+  TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + h * ar.G + (rr - i * ar.G)) * D;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    if constexpr (std::is_same<TQ, __half>::value)
+      dst[e * 32 + lane] = __float2half_rn(o[e] * inv);
+    else
+      dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+  }
+}
+
+}  // namespace tcore
+}  // namespace kv8
+}  // namespace wq
+
+namespace wq_host {
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct TcWs {
+  size_t ml, prefix, bytes;
+};
+TcWs tc_ws(int64_t B, int64_t max_rows, int64_t D, bool pair) {
+  const size_t rows = pair ? 256 : 128, w2 = size_t(sm_count()) * 2;
+  TcWs s;
+  s.ml = up256(w2 * rows * size_t(D) * 4);
+  s.prefix = s.ml + up256(w2 * rows * 8);
+  s.bytes = s.prefix + up256(size_t(B * ((max_rows + int64_t(rows) - 1) / int64_t(rows)) + 1) * 8);
+  return s;
+}
+
+template <typename TQ, int FMT, int D, bool PAIR>
+int launch_tc(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int max_pos, float scale,
+              void* out, uint8_t* ws, cudaStream_t s) {
+  using namespace wq::kv8;
+  using namespace wq::kv8::tcore;
+  auto kern = attn_kv8_tc_kernel<TQ, FMT, D, PAIR>;
+  constexpr size_t smem = Smem<D>::BYTES;
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  WQ_CUDA_CHECK(cudaGetDevice(&dev));
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      WQ_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  constexpr int64_t ROWS = PAIR ? 256 : 128;
+  int tshift = 0;
+  while ((int64_t(1) << tshift) < a.page) ++tshift;
+  const int G = int(heads / a.kv_heads);
+  const int64_t most_r = (a.max_new * G + ROWS - 1) / ROWS;
+  if (a.B * most_r > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
+  const Cache c{static_cast<uint8_t*>(a.kq), a.ks, static_cast<uint8_t*>(a.vq), a.vs, a.pages,
+                int(a.kv_heads), tshift};
+  const Batch bt{a.table, a.cu, a.lens, int(a.B), int(a.width), int(a.rows), int(a.max_new)};
+  const Rope rp{a.cos, a.sin, int(a.rot), max_pos, a.interleaved};
+  const TcWs w = tc_ws(a.B, a.max_new * G, D, PAIR);
+  const TcArgs ar{ldq, int(heads), G, int(most_r), scale * 1.4426950408889634f,
+                  reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
+                  reinterpret_cast<int64_t*>(ws + w.prefix)};
+  const int grid = sm_count();
+  TQ* o = static_cast<TQ*>(out);
+  kern<<<grid, THREADS, smem, s>>>(static_cast<const TQ*>(Q), o, c, bt, rp, ar, status_ptr(),
+                                   wait_limit_ns());
+  WQ_LAUNCH_CHECK("attn_kv8_tc_kernel");
+  if (grid < 2) return WQ_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((grid - 1) * (ROWS / 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_tc_join_kernel<TQ, D, PAIR>, o, c, bt, ar,
+                                   int64_t(grid)));
+  return WQ_OK;
+}
+
+template <int FMT, int D>
+int launch_tc_by_type(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
+                      int max_pos, float scale, void* out, uint8_t* ws, cudaStream_t s) {
+  if (dtype == WQ_F16)
+    return launch_tc<__half, FMT, D, false>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
+  if (attn_kv8_pairs(dtype, heads, a.kv_heads, a.max_new))
+    return launch_tc<__nv_bfloat16, FMT, D, true>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
+  return launch_tc<__nv_bfloat16, FMT, D, false>(Q, ldq, heads, a, max_pos, scale, out, ws, s);
+}
+
+}  // namespace
+
+// Whether the tensor-memory kernel takes the call: more than 8 rows to a
+// (sequence, kv head), heads of 64 or 128.
+bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
+  return D <= 128 && max_q * (heads / kv_heads) > 8;
+}
+bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
+  return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
+}
+
+size_t attn_kv8_tc_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                   int64_t max_q) {
+  const int64_t rows = max_q * (heads / kv_heads);
+  const size_t one = tc_ws(B, rows, D, false).bytes;
+  const size_t two = rows > 128 ? tc_ws(B, rows, D, true).bytes : 0;
+  return one > two ? one : two;
+}
+
+int launch_attn_kv8_tc(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
+                       int max_pos, float scale, void* out, void* ws, cudaStream_t s) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const bool i8 = a.fmt == WQ_W8_INT8;
+  if (a.D == 64)
+    return i8 ? launch_tc_by_type<WQ_W8_INT8, 64>(Q, dtype, ldq, heads, a, max_pos, scale, out, w, s)
+              : launch_tc_by_type<WQ_W8_E4M3, 64>(Q, dtype, ldq, heads, a, max_pos, scale, out, w, s);
+  return i8 ? launch_tc_by_type<WQ_W8_INT8, 128>(Q, dtype, ldq, heads, a, max_pos, scale, out, w, s)
+            : launch_tc_by_type<WQ_W8_E4M3, 128>(Q, dtype, ldq, heads, a, max_pos, scale, out, w, s);
+}
+
+}  // namespace wq_host

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
         const uint32_t buf = it & 1u;
         const uint64_t s2 = pair(s, s);
         if (kb + 1 < kblocks) s = __ldg(sxp + (kb + 1) * ldsx) * __ldg(swp + kb + 1);
-        if (!(ok = tc::wait_bounded(&sm.tfull[buf], (it >> 1) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.tfull[buf], (it >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -221,7 +221,7 @@ struct Split {
   static constexpr int BUFS = 4;
   static constexpr uint32_t TMEM = NT * BUFS < 32 ? 32 : NT * BUFS;
   struct Bars {
-    uint64_t full[STAGES], empty[STAGES], tfull[BUFS], tempty[BUFS], drain;
+    uint64_t full[STAGES], empty[STAGES], tfull[BUFS], tempty[BUFS], parts, told, drain;
     uint32_t tmem_base;
     int abort_flag, last;
   };
@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
       tc::mbar_init(&sm.tfull[b], 1);
       tc::mbar_init(&sm.tempty[b], P::EWARPS);
     }
+    tc::mbar_init(&sm.parts, P::EWARPS);
+    tc::mbar_init(&sm.told, 1);
     tc::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     tc::fence_mbar_init();
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
     const int et = threadIdx.x - 64;          // epilogue thread
     int it = 0;
     int slot = 0;
+    uint32_t cuts = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
       const int tile = int(u / kblocks);
@@ -370,8 +373,8 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         const float wk = w;
         if (u + 1 < e) w = __ldg(++swp);
         // both, so that the scales (written by the copy) are seen as well
-        if (!(ok = tc::wait_bounded(&sm.full[s], (it / P::STAGES) & 1u, wd))) break;
-        if (!(ok = tc::wait_bounded(&sm.tfull[buf], (it / P::BUFS) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.full[s], (it / P::STAGES) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.tfull[buf], (it / P::BUFS) & 1u, wd))) break;
         tc::fence_after_sync();
         const uint32_t taddr =
             tmem + (uint32_t(q * 32) << 16) + buf * NT + uint32_t(cg) * P::COLS;
@@ -411,10 +414,18 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < P::COLS; ++j) __stcg(dst + j * 128, acc[j]);
         __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"r"(P::EWARPS * 32) : "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.parts);
         const int c0 = owner(t0, U, G), c1 = owner(t1 - 1, U, G);
-        if (et == 0) sm.last = atomicAdd(counters + tile, 1) == c1 - c0;
-        asm volatile("bar.sync 1, %0;" ::"r"(P::EWARPS * 32) : "memory");
+        if (et < 32) {
+          if (!(ok = tc::wait_warp(&sm.parts, cuts & 1u, wd))) break;
+          if (lane == 0) {
+            sm.last = atomicAdd(counters + tile, 1) == c1 - c0;
+            tc::mbar_arrive(&sm.told);
+          }
+        }
+        if (!(ok = tc::wait_warp(&sm.told, cuts & 1u, wd))) break;
+        ++cuts;
         if (!sm.last) continue;
         __threadfence();
 #pragma unroll

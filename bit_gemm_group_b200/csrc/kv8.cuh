@@ -103,5 +103,32 @@ __device__ __forceinline__ void rotated8(const T* row, int d, int pos, const Rop
   }
 }
 
+// The one-pass softmax of both attention kernels (its scheme: attn_kv8.cu).
+constexpr float LAG = 8.f;  // how far a maximum may grow before the sums are rescaled
+constexpr float OFF = 6.f;  // weights are kept 2^OFF above their exponential
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Units [u0, u1) of worker w: [w U / W, (w + 1) U / W).
+__device__ __forceinline__ int64_t run_start(int64_t w, int64_t U, int64_t W) { return w * U / W; }
+__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t U, int64_t W) {
+  return ((u + 1) * W - 1) / U;
+}
+// Workers in use: no run is shorter than two units (a cut run costs a part in
+// the workspace, about a unit's bytes).
+__device__ __forceinline__ int64_t workers(int64_t U, int64_t W) {
+  const int64_t w = (U + 1) / 2;
+  return w < W ? w : W;
+}
+
 }  // namespace kv8
 }  // namespace wq

@@ -95,6 +95,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
   }
 }
 
+// wait_bounded by a whole warp with one answer, so that the warp stays together
+// for the warp-wide instructions that follow.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, wd));
+}
+
 // Drain wait used while a kernel shuts down: ignores the abort flag, gives up
 // silently at `deadline_ns`.
 __device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
