@@ -31,6 +31,7 @@ WQ_ERR_WORKSPACE = -8
 WQ_ERR_NO_DEVICE = -9
 
 WQ_F32, WQ_BF16, WQ_F16 = 0, 1, 2
+WQ_W8_INT8, WQ_W8_E4M3 = 0, 1
 
 # every symbol include/wq.h declares
 EXPORTED = (
@@ -366,9 +367,6 @@ def wq_gemm_fp8(X, Wq, w_scales, Y, ws, acc_out=None, stream=None):
     _check(st, "wq_gemm_fp8")
 
 
-WQ_W8_INT8, WQ_W8_E4M3 = 0, 1
-
-
 def wq_gemm_w8a16(X, Wq, w_fmt, w_scales, Y, stream=None):
     M, K = X.shape
     N = Wq.shape[0]
@@ -380,44 +378,83 @@ def wq_gemm_w8a16(X, Wq, w_fmt, w_scales, Y, stream=None):
     _check(st, "wq_gemm_w8a16")
 
 
-def _same_device(*tensors):
-    """The device that all of the tensors are on; a call's pointers belong to one."""
+def _device(*tensors):
+    """Index of the device that all of the tensors are on (a call's pointers belong to one)."""
     dev = None
     for t in tensors:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("expected a torch.Tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise WQError(WQ_ERR_ARG, f"tensors on {dev} and {t.device}")
+        try:
+            d = t.get_device()
+        except AttributeError:
+            raise TypeError("expected a torch.Tensor") from None
+        if d != dev:
+            if dev is not None:
+                raise WQError(WQ_ERR_ARG, f"tensors on devices {dev} and {d} (-1: CPU)")
+            dev = d
+    if dev is None or dev < 0:
+        raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
     return dev
 
 
-def _typed(t, dtype, what):
-    if isinstance(t, torch.Tensor) and t.dtype != dtype:
+def _holds(t, dtype, count, what):
+    """The tensor, refused unless it has `count` elements of `dtype`."""
+    if t.dtype != dtype:
         raise WQError(WQ_ERR_ARG, f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() < count:
+        raise WQError(WQ_ERR_ARG, f"{what} holds {t.numel()} elements, the call needs {count}")
     return t
 
 
-def _on(dev):
-    """Make `dev` current for a call: the library works on the current device."""
-    if dev.type != "cuda":
+def _addr(t):
+    """Address of a contiguous tensor (its device has been checked)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise WQError(WQ_ERR_ARG, "tensor must be contiguous (row-major)")
+    return t.data_ptr()
+
+
+def _call(dev, name, stream, *args):
+    """Call an entry point on device `dev` (the library works on the current one), on its
+    current stream unless given."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != WQ_OK:
+        raise WQError(st, name)
+
+
+# handle of the current stream of a device (torch.cuda.current_stream builds an object,
+# which costs a microsecond of every call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _workspace(like, name, *sizes):
+    """An uninitialised workspace on the device of `like`, of the size that `name` says."""
+    dev = like.get_device()
+    if dev < 0:
         raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
-    return torch.cuda.device(dev)
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        n = fn(*sizes)
+    else:
+        with torch.cuda.device(dev):
+            n = fn(*sizes)
+    return like.new_empty((max(1, n),), dtype=torch.uint8)
 
 
 def wq_quantize_fp8_block(A, block_rows, q, scales, stream=None):
     R, K = A.shape
-    KB = -(-K // 128)
     _fits(q, R * K, "q")
-    _fits(_typed(scales, torch.float32, "scales"),
-          4 * KB * (-(-R // block_rows) if block_rows > 0 else 0), "scales")
-    with _on(_same_device(A, q, scales)):
-        st = lib().wq_quantize_fp8_block(_ptr(A), _DTYPE_TAG.get(A.dtype, -1), R, K, block_rows,
-                                         _ptr(q), _ptr(scales), _stream(stream))
-    _check(st, "wq_quantize_fp8_block")
+    _holds(scales, torch.float32, -(-K // 128) * (-(-R // block_rows) if block_rows > 0 else 0),
+           "scales")
+    _call(_device(A, q, scales), "wq_quantize_fp8_block", stream, _addr(A),
+          _DTYPE_TAG.get(A.dtype, -1), R, K, block_rows, _addr(q), _addr(scales))
 
 
 def wq_fp8_block_workspace_bytes(M, N, K):
@@ -426,29 +463,26 @@ def wq_fp8_block_workspace_bytes(M, N, K):
 
 def wq_gemm_fp8_block(X, Wq, w_scales, Y, ws, stream=None):
     M, K = X.shape
-    N, KB = Wq.shape[0], -(-K // 128)
+    N = Wq.shape[0]
+    _holds(X, torch.bfloat16, 0, "X")
+    _holds(Y, torch.bfloat16, M * N, "Y")
     _fits(Wq, N * K, "Wq")
-    _fits(_typed(w_scales, torch.float32, "w_scales"), 4 * -(-N // 128) * KB, "w_scales")
-    _fits(Y, 2 * M * N, "Y")
-    with _on(_same_device(X, Wq, w_scales, Y, ws)):
-        st = lib().wq_gemm_fp8_block(_bf16(X, "X"), M, K, _ptr(Wq), _ptr(w_scales), N,
-                                     _bf16(Y, "Y"), _ptr(ws), ws.numel() * ws.element_size(),
-                                     _stream(stream))
-    _check(st, "wq_gemm_fp8_block")
+    _holds(w_scales, torch.float32, -(-N // 128) * -(-K // 128), "w_scales")
+    _call(_device(X, Wq, w_scales, Y, ws), "wq_gemm_fp8_block", stream, _addr(X), M, K, _addr(Wq),
+          _addr(w_scales), N, _addr(Y), _addr(ws), ws.numel() * ws.element_size())
 
 
-def _rows_ptr(t, what):
-    """(pointer, elements between rows) of a [n, heads, D] tensor whose rows may be
-    columns of a wider one (a slice of a fused projection's output)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("expected a torch.Tensor")
-    if not t.is_cuda:
-        raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
+def _row_stride(t, what):
+    """Elements between the rows of a [n, heads, D] tensor, whose rows may be columns of a
+    wider one (a slice of a fused projection's output)."""
     n, heads, D = t.shape
-    ld = t.stride(0) if n > 1 else heads * D
-    if t.numel() and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+    ld, between, one = t.stride()
+    if n and (one != 1 or (heads > 1 and between != D)):
         raise WQError(WQ_ERR_ARG, f"{what}: the heads of a row must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return ld if n > 1 else heads * D
+
+
+_KV8_FORMAT = {torch.int8: WQ_W8_INT8, torch.uint8: WQ_W8_E4M3, torch.float8_e4m3fn: WQ_W8_E4M3}
 
 
 def _kv8_args(cache, heads, D, block_table, cu_rows, seq_lens, max_new, rope):
@@ -457,30 +491,27 @@ def _kv8_args(cache, heads, D, block_table, cu_rows, seq_lens, max_new, rope):
     kq, ks, vq, vs = cache
     if kq.dim() != 4 or kq.shape != vq.shape or kq.dtype != vq.dtype:
         raise WQError(WQ_ERR_ARG, "cache: kq and vq must be [pages, heads, page_size, D], alike")
-    if kq.dtype not in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+    fmt = _KV8_FORMAT.get(kq.dtype)
+    if fmt is None:
         raise WQError(WQ_ERR_ARG, f"cache: codes must be int8, or uint8 for E4M3, got {kq.dtype}")
     P, kv, T, cd = kq.shape
     if cd != D:
         raise WQError(WQ_ERR_ARG, f"cache holds heads of {cd} elements, the rows of {D}")
-    for t, what in ((ks, "ks"), (vs, "vs")):
-        _fits(_typed(t, torch.float32, what), 4 * P * kv, what)
-    for t, what in ((block_table, "block_table"), (cu_rows, "cu_rows"), (seq_lens, "seq_lens")):
-        _typed(t, torch.int32, what)
-    B, width = block_table.shape
-    _fits(cu_rows, 4 * (B + 1), "cu_rows")
-    _fits(seq_lens, 4 * B, "seq_lens")
-    cos, sin, inter = (None, None, False) if rope is None else rope
-    rot, max_pos = 0, 0
-    if cos is not None:
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        if sin is None or sin.shape != cos.shape:
+    _holds(ks, torch.float32, P * kv, "ks")
+    _holds(vs, torch.float32, P * kv, "vs")
+    B, width = _holds(block_table, torch.int32, 0, "block_table").shape
+    _holds(cu_rows, torch.int32, B + 1, "cu_rows")
+    _holds(seq_lens, torch.int32, B, "seq_lens")
+    cos, sin, inter, rot, max_pos = None, None, False, 0, 0
+    if rope is not None:
+        cos, sin, inter = rope
+        max_pos, half = _holds(cos, torch.float32, 0, "cos").shape
+        rot = 2 * half
+        if _holds(sin, torch.float32, 0, "sin").shape != cos.shape:
             raise WQError(WQ_ERR_ARG, "cos and sin must have the same shape")
-        _typed(cos, torch.float32, "cos")
-        _typed(sin, torch.float32, "sin")
-    fmt = WQ_W8_INT8 if kq.dtype == torch.int8 else WQ_W8_E4M3
-    return [kv, D, fmt, _ptr(kq), _ptr(ks), _ptr(vq), _ptr(vs), P, T, _ptr(block_table), width,
-            _ptr(cu_rows), _ptr(seq_lens), B, int(max_new), _ptr(cos), _ptr(sin), rot, max_pos,
-            int(bool(inter))]
+    return (kv, D, fmt, _addr(kq), _addr(ks), _addr(vq), _addr(vs), P, T, _addr(block_table),
+            width, _addr(cu_rows), _addr(seq_lens), B, max_new, _addr(cos), _addr(sin), rot,
+            max_pos, 1 if inter else 0)
 
 
 def wq_kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope=None, stream=None):
@@ -490,12 +521,10 @@ def wq_kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope=Non
     if cache[0].dim() == 4 and cache[0].shape[1] != heads:
         raise WQError(WQ_ERR_ARG, f"cache has {cache[0].shape[1]} heads, K has {heads}")
     cos, sin = (None, None) if rope is None else rope[:2]
-    with _on(_same_device(K, V, *cache, block_table, cu_rows, seq_lens, cos, sin)):
-        (kp, ldk), (vp, ldv) = _rows_ptr(K, "K"), _rows_ptr(V, "V")
-        st = lib().wq_kv8_append(kp, vp, _DTYPE_TAG.get(K.dtype, -1), n, ldk, ldv,
-                                 *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens,
-                                            max_new, rope), _stream(stream))
-    _check(st, "wq_kv8_append")
+    dev = _device(K, V, *cache, block_table, cu_rows, seq_lens, cos, sin)
+    _call(dev, "wq_kv8_append", stream, K.data_ptr(), V.data_ptr(), _DTYPE_TAG.get(K.dtype, -1), n,
+          _row_stride(K, "K"), _row_stride(V, "V"),
+          *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens, max_new, rope))
 
 
 def wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new):
@@ -505,17 +534,13 @@ def wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new):
 def wq_attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new, scale, out, ws, rope=None,
                 stream=None):
     n, heads, D = Q.shape
-    if out.dtype != Q.dtype:
-        raise WQError(WQ_ERR_ARG, f"out must be {Q.dtype}, got {out.dtype}")
-    _fits(out, Q.numel() * Q.element_size(), "out")
+    _holds(out, Q.dtype, n * heads * D, "out")
     cos, sin = (None, None) if rope is None else rope[:2]
-    with _on(_same_device(Q, *cache, block_table, cu_rows, seq_lens, out, ws, cos, sin)):
-        qp, ldq = _rows_ptr(Q, "Q")
-        st = lib().wq_attn_kv8(qp, _DTYPE_TAG.get(Q.dtype, -1), n, ldq, heads,
-                               *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens,
-                                          max_new, rope), float(scale), _ptr(out), _ptr(ws),
-                               ws.numel() * ws.element_size(), _stream(stream))
-    _check(st, "wq_attn_kv8")
+    dev = _device(Q, *cache, block_table, cu_rows, seq_lens, out, ws, cos, sin)
+    _call(dev, "wq_attn_kv8", stream, Q.data_ptr(), _DTYPE_TAG.get(Q.dtype, -1), n,
+          _row_stride(Q, "Q"), heads,
+          *_kv8_args(cache, heads, D, block_table, cu_rows, seq_lens, max_new, rope), scale,
+          _addr(out), _addr(ws), ws.numel() * ws.element_size())
 
 
 def wq_gptq_quantize(W, U, group_size, sym, codes, scales, zeros, ws, stream=None):
@@ -691,8 +716,8 @@ def quantize_fp8_block(A, block_rows=128):
     """E4M3 codes uint8 [R, K] and fp32 scales [ceil(R / block_rows), ceil(K / 128)]:
     block_rows 128 for a weight, 1 for activations."""
     R, K = A.shape
-    q = torch.empty((R, K), dtype=torch.uint8, device=A.device)
-    s = torch.empty((-(-R // block_rows), -(-K // 128)), dtype=torch.float32, device=A.device)
+    q = A.new_empty((R, K), dtype=torch.uint8)
+    s = A.new_empty((-(-R // block_rows), -(-K // 128)), dtype=torch.float32)
     wq_quantize_fp8_block(A, block_rows, q, s)
     return q, s
 
@@ -703,11 +728,9 @@ def gemm_fp8_block(X, Wq, w_scales, ws=None):
     wq_fp8_block_workspace_bytes(M, N, K) bytes to reuse from call to call."""
     M, K = X.shape
     N = Wq.shape[0]
-    Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+    Y = X.new_empty((M, N))
     if ws is None:
-        with _on(X.device):
-            n = wq_fp8_block_workspace_bytes(M, N, K)
-        ws = torch.empty((max(1, n),), dtype=torch.uint8, device=X.device)
+        ws = _workspace(X, "wq_fp8_block_workspace_bytes", M, N, K)
     wq_gemm_fp8_block(X, Wq, w_scales, Y, ws)
     return Y
 
@@ -733,21 +756,20 @@ def kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope=None):
     wq_kv8_append(K, V, cache, block_table, cu_rows, seq_lens, max_new, rope)
 
 
-def attn_kv8_workspace(B, heads, kv_heads, D, max_new, device):
+def attn_kv8_workspace(B, heads, kv_heads, D, max_new, device="cuda"):
     """A workspace for attn_kv8, to be reused from call to call on one stream."""
-    with _on(torch.empty(0, device=device).device):
-        n = wq_attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new)
-    return torch.empty((max(1, n),), dtype=torch.uint8, device=device)
+    return _workspace(torch.empty(0, device=device), "wq_attn_kv8_workspace_bytes", B, heads,
+                      kv_heads, D, max_new)
 
 
 def attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new, scale=None, rope=None, ws=None):
     """Causal attention of Q [n, heads, D] over the paged cache (after the rows' append,
     with the same cu_rows and seq_lens): [n, heads, D].  scale: 1 / sqrt(D) by default."""
     n, heads, D = Q.shape
-    out = torch.empty((n, heads, D), dtype=Q.dtype, device=Q.device)
+    out = Q.new_empty((n, heads, D))
     if ws is None:
-        ws = attn_kv8_workspace(block_table.shape[0], heads, cache[0].shape[1], D, max_new,
-                                Q.device)
+        ws = _workspace(Q, "wq_attn_kv8_workspace_bytes", block_table.shape[0], heads,
+                        cache[0].shape[1], D, max_new)
     wq_attn_kv8(Q, cache, block_table, cu_rows, seq_lens, max_new,
                 D ** -0.5 if scale is None else scale, out, ws, rope)
     return out

@@ -111,21 +111,28 @@ __global__ void __launch_bounds__(512)
       *reinterpret_cast<uint32_t*>(codes + i) = o;
     }
   }
-  const float inv = rcp_approx(s), top = s * TOP;
+  const float inv = __frcp_rn(s), top = s * TOP;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int r = first + i * rstep;
     if (r >= rows) break;
-    uint32_t o[2] = {0, 0};
+    uint32_t o[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = fminf(fmaxf(x[i][e], -top), top);
-      uint32_t y;
-      if (FMT == WQ_W8_INT8)
-        y = uint32_t(uint8_t(code_i8_exact(v, s, inv)));
-      else
-        y = __nv_cvt_float_to_fp8(quot_e4m3(v, s, inv), __NV_SATFINITE, __NV_E4M3);
-      o[e >> 2] |= y << (8 * (e & 3));
+    for (int k = 0; k < 2; ++k) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = quot_rn(fminf(fmaxf(x[i][4 * k + e], -top), top), s, inv);
+      if (FMT == WQ_W8_INT8) {
+        // the low byte of v + 1.5 2^23 is v rounded half to even
+        const float magic = 12582912.f;
+        o[k] = low_bytes4(__float_as_uint(v[0] + magic), __float_as_uint(v[1] + magic),
+                          __float_as_uint(v[2] + magic), __float_as_uint(v[3] + magic));
+      } else {
+        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+        o[k] = a | (b << 16);
+      }
     }
     *reinterpret_cast<uint2*>(codes + int64_t(slot0 + r) * D + d) = make_uint2(o[0], o[1]);
   }

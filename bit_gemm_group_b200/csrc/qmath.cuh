@@ -72,6 +72,23 @@ __device__ __forceinline__ float quot_e4m3(float x, float s, float inv) {
   return r;
 }
 
+// fl(x / s) without a division or a branch, from y = fl(1 / s) (__frcp_rn):
+// Markstein's method (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990): where y is the
+// correctly rounded reciprocal and q is within one unit of the last place of
+// x / s, fl(q + (x - q s) y) is fl(x / s); the remainder is exact in one fma.
+// x y is within 2^-23 of x / s in relation to it, which may be two units, so a
+// first such step brings it within one and a second rounds it.  The remainders
+// are exact while |x| > 2^-76 (below that, with s >= 1e-8, every 8-bit code is
+// 0 either way).  Five instructions of the fma pipe, where deciding only the
+// quotients near half-way costs more on the half-rate integer pipe: two 16-bit
+// floats often have a quotient that is a tie of the 8-bit grid.
+__device__ __forceinline__ float quot_rn(float x, float s, float y) {
+  float q = x * y;
+  q = fmaf(fmaf(-q, s, x), y, q);
+  return fmaf(fmaf(-q, s, x), y, q);
+}
+
 // The largest |x| (sym) or the smallest and largest x (asym) of a lane's 16
 // 16-bit elements, on the packed pairs.  NaN propagates (.NaN), so a lane
 // with a NaN or an infinity yields a non-finite statistic.

@@ -20,26 +20,25 @@ namespace fp8b {
 constexpr int THREADS = 256;
 constexpr int STEPS = 8;  // 16 rows each
 
+// Eight elements of a row, as loaded.  absmax: the largest magnitude, non-finite
+// if one of them is.
 template <typename T>
-struct Row8;
-template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-};
-template <typename T>
-struct Row8 {
+struct Row8 {  // 16-bit
+  static constexpr int CTAS = 4;
   uint4 v;
   __device__ void load(const T* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ uint32_t absmax(uint32_t m) const {
+    m = absmax2<T>(m, v.x);
+    m = absmax2<T>(m, v.y);
+    m = absmax2<T>(m, v.z);
+    return absmax2<T>(m, v.w);
+  }
+  static __device__ float value(uint32_t m) {
+    float a, b;
+    unpack2<T>(m & 0x7FFF7FFFu, a, b);
+    return a > b || a != a ? a : b;
+  }
   __device__ void get(float (&x)[8]) const {
     unpack2<T>(v.x, x[0], x[1]);
     unpack2<T>(v.y, x[2], x[3]);
@@ -47,26 +46,49 @@ struct Row8 {
     unpack2<T>(v.w, x[6], x[7]);
   }
 };
-
-// Largest |x| of 8 elements, NaN skipped; `bad` is raised by any non-finite one.
-__device__ __forceinline__ float absmax8(const float (&x)[8], bool& bad) {
-  float m = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    m = fmaxf(m, fabsf(x[e]));
-    bad |= !(fabsf(x[e]) <= 3.4028234663852886e38f);
+template <>
+struct Row8<float> {
+  static constexpr int CTAS = 2;
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
-  return m;
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ uint32_t absmax(uint32_t m) const {
+    float x[8];
+    get(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ float value(uint32_t m) { return __uint_as_float(m); }
+  __device__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+
+// The larger of two magnitudes (>= 0, infinite or NaN): a NaN's pattern is the
+// largest.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 
-// Eight codes of x / s.  The quotients come from one reciprocal
-// (quot_e4m3: the IEEE quotient's code, the division itself near half-way).
+// max(a / 448, 1e-8); of a block with a non-finite element, that.
+__device__ __forceinline__ float scale_of(float a, bool& bad) {
+  if (__float_as_uint(a) < 0x7F800000u) return fmaxf(div_rn(a, 448.f), 1e-8f);
+  bad = true;
+  return a;
+}
+
+// Eight codes of x / s, from inv = fl(1 / s).
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv) {
   uint32_t h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 v = make_float2(quot_e4m3(x[2 * j], s, inv), quot_e4m3(x[2 * j + 1], s, inv));
-    h[j] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    const float2 r = make_float2(quot_rn(x[2 * j], s, inv), quot_rn(x[2 * j + 1], s, inv));
+    h[j] = __nv_cvt_float2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
@@ -75,7 +97,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv)
 // [KB, ld] with `transposed` (the layout the product reads).  `counters`
 // (nullable): n_counters words of the product's workspace set to zero.
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, Row8<T>::CTAS)
     quantize_fp8_block_kernel(const T* __restrict__ X, int64_t R, int64_t K, uint8_t* __restrict__ q,
                               float* __restrict__ scales, int64_t ld, bool transposed,
                               int* __restrict__ counters, int n_counters, int* status) {
@@ -85,63 +107,60 @@ __global__ void __launch_bounds__(THREADS)
   const int64_t tile = blockIdx.x;
   const int kb = int(tile % KB);
   const int64_t r0 = (tile / KB) * 128;
-  const int c8 = (threadIdx.x & 15) * 8;
-  const int64_t k = int64_t(kb) * 128 + c8;
-  const int64_t row = r0 + (threadIdx.x >> 4);
+  // row and column of piece i
+  const int64_t row0 = r0 + (ROWS == 1 ? threadIdx.x >> 2 : threadIdx.x >> 4);
+  const int64_t k0 = int64_t(kb) * 128 + (ROWS == 1 ? threadIdx.x & 3 : threadIdx.x & 15) * 8;
+  auto row_of = [&](int i) { return row0 + (ROWS == 1 ? (i >> 2) * 64 : i * 16); };
+  auto col_of = [&](int i) { return k0 + (ROWS == 1 ? (i & 3) * 32 : 0); };
   for (int i = int(tile) * THREADS + threadIdx.x; i < n_counters; i += int(gridDim.x) * THREADS)
     counters[i] = 0;
 
   Row8<T> v[STEPS];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    const int64_t r = row + 16 * i;
-    if (r < R && k < K)
-      v[i].load(X + r * K + k);
+    if (row_of(i) < R && col_of(i) < K)
+      v[i].load(X + row_of(i) * K + col_of(i));
     else
       v[i].zero();
   }
   bool bad = false;
-  float m[STEPS];
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    float x[8];
-    v[i].get(x);
-    m[i] = absmax8(x, bad);
-  }
+  float s[2], inv[2];  // of pieces 0 to 3 and 4 to 7
   if (ROWS == 128) {
-    float a = m[0];
+    uint32_t a = 0;
 #pragma unroll
-    for (int i = 1; i < STEPS; ++i) a = fmaxf(a, m[i]);
-    a = warp_max(a);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    for (int i = 0; i < STEPS; ++i) a = v[i].absmax(a);
+    float f = Row8<T>::value(a);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f = max_mag(f, __shfl_xor_sync(0xffffffffu, f, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = f;
     __syncthreads();
-    a = red[0];
 #pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w) a = fmaxf(a, red[w]);
-    const float s = fmaxf(div_rn(a, 448.f), 1e-8f);
-    if (threadIdx.x == 0) scales[(r0 / 128) * KB + kb] = s;
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) m[i] = s;
+    for (int w = 0; w < THREADS / 32; ++w) f = max_mag(f, red[w]);
+    s[0] = s[1] = scale_of(f, bad);
+    if (threadIdx.x == 0) scales[(r0 / 128) * KB + kb] = s[0];
   } else {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
+    for (int j = 0; j < 2; ++j) {
+      uint32_t a = 0;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
-      m[i] = fmaxf(div_rn(m[i], 448.f), 1e-8f);
-      const int64_t r = row + 16 * i;
-      if ((threadIdx.x & 15) == 0 && r < R)
-        scales[transposed ? int64_t(kb) * ld + r : r * ld + kb] = m[i];
+      for (int i = 0; i < 4; ++i) a = v[4 * j + i].absmax(a);
+      float f = Row8<T>::value(a);
+#pragma unroll
+      for (int o = 2; o > 0; o >>= 1) f = max_mag(f, __shfl_xor_sync(0xffffffffu, f, o));
+      s[j] = scale_of(f, bad);
+      const int64_t r = row_of(4 * j);
+      if ((threadIdx.x & 3) == 0 && r < R)
+        scales[transposed ? int64_t(kb) * ld + r : r * ld + kb] = s[j];
     }
   }
-  float inv = ROWS == 128 ? rcp_approx(m[0]) : 0.f;
+  inv[0] = __frcp_rn(s[0]);
+  inv[1] = ROWS == 128 ? inv[0] : __frcp_rn(s[1]);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    const int64_t r = row + 16 * i;
-    if (r >= R || k >= K) continue;
+    if (row_of(i) >= R || col_of(i) >= K) continue;
     float x[8];
     v[i].get(x);
-    if (ROWS == 1) inv = rcp_approx(m[i]);
-    *reinterpret_cast<uint2*>(q + r * K + k) = codes8(x, m[i], inv);
+    *reinterpret_cast<uint2*>(q + row_of(i) * K + col_of(i)) = codes8(x, s[i >> 2], inv[i >> 2]);
   }
   if (bad) record_error(status, WQ_ERR_NONFINITE);
 }
