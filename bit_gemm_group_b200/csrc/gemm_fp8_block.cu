@@ -34,7 +34,11 @@ constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS_L = 32 * (2 + EPI_WARPS);
+// warps 0 to 3 copy and issue, 4 to 11 add: 168 registers a thread at launch,
+// split 56 to 224 (128 sums and two chunks of 32 on their way)
+constexpr int THREADS_L = 32 * (4 + EPI_WARPS);
+constexpr int REGS_ISSUE = 56, REGS_ADD = 224;
+static_assert(4 * REGS_ISSUE + EPI_WARPS * REGS_ADD <= (4 + EPI_WARPS) * 168, "registers");
 constexpr uint32_t IDESC_L = tc::idesc_e4m3_f32(BM, BN);
 
 struct SmemL {
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
   // the quantizer's codes and scales of X are complete from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
 
   if (warp == 0) {
     if (lane == 0) {
@@ -149,9 +154,10 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       tc::mma_commit(&sm.drain);
       tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
-  } else {
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ADD));
     const int q = warp & 3;           // tensor-memory lane quarter
-    const int half = (warp - 2) >> 2;  // channels [128 half, 128 half + 128) of the tile
+    const int half = (warp - 4) >> 2;  // channels [128 half, 128 half + 128) of the tile
     uint32_t it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
@@ -164,25 +170,36 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      float s = __ldg(sxp) * __ldg(swp);
+      // scales two K blocks ahead
+      auto scale_at = [&](int kb) {
+        const int k = kb < kblocks ? kb : kblocks - 1;
+        return __ldg(sxp + k * ldsx) * __ldg(swp + k);
+      };
+      float s0 = scale_at(0), s1 = scale_at(1);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        const uint64_t s2 = pair(s, s);
-        if (kb + 1 < kblocks) s = __ldg(sxp + (kb + 1) * ldsx) * __ldg(swp + kb + 1);
+        const uint64_t s2 = pair(s0, s0);
+        s0 = s1;
+        s1 = scale_at(kb + 2);
         if (!(ok = tc::wait_warp(&sm.tfull[buf], (it >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
+        // a chunk of 32 channels is on its way while the one before is added
+        const uint32_t t = taddr + buf * BN;
+        uint32_t r[2][32];
+        tc::tmem_ld_x32(t, r[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t r[16];
-          tc::tmem_ld_x16(taddr + buf * BN + c * 16, r);
+        for (int c = 0; c < 4; ++c) {
           tc::tmem_wait_ld();
-          if (c == 7) {
+          if (c < 3) {
+            tc::tmem_ld_x32(t + (c + 1) * 32, r[(c + 1) & 1]);
+          } else {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.tempty[buf]);
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) fma2(acc[c * 8 + j], r[2 * j], r[2 * j + 1], s2);
+          for (int j = 0; j < 16; ++j)
+            fma2(acc[c * 16 + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], s2);
         }
       }
       if (ok && row < M) {

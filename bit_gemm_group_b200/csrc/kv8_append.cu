@@ -10,14 +10,23 @@
 // Bound by HBM: 2 (4) bytes read and 1 written per element.  One CTA per
 // (sequence, touched page, head, keys or values) holds the page's new rows in
 // registers between the maximum and the codes, so a block is read once and its
-// scale is written by one CTA, with no atomics.  In a decode step a CTA has one
-// row; older codes are read only when the new row raises the maximum.
+// scale is written by one CTA, with no atomics.  A thread's piece is 16
+// elements of a row that rotate with one another (8 and their 8 partners), so
+// that nothing is read twice; the loads of its four pieces are in flight
+// together.  In a decode step a CTA has one row; older codes are read only when
+// the new row raises the maximum.
 #include "kv8.cuh"
 
 namespace wq {
 namespace kv8 {
 
-constexpr int STEPS = 8;  // 8-element pieces per thread; T D / 64 threads
+constexpr int STEPS = 4;  // 16-element pieces per thread; T D / 64 threads
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = u;
+}
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(512)
@@ -50,28 +59,58 @@ __global__ void __launch_bounds__(512)
     return;
   }
   const int slot0 = p0 & (T_ - 1), rows = p1 - p0;
-  const int per = D >> 3;                       // pieces per row
-  const int d = int(threadIdx.x % per) * 8;
+  const int per = D >> 4;                       // pieces per row
+  const int piece = int(threadIdx.x) % per;
   const int first = int(threadIdx.x) / per, rstep = int(blockDim.x) / per;
+  // the piece's two runs of 8 elements, and where its angles are
+  const int half = rp.rot >> 1;
+  const bool turns = !is_v && rp.cos != nullptr && piece * 16 < rp.rot;
+  const bool split = turns && !rp.interleaved;
+  const int d0 = split ? piece * 8 : piece * 16, d1 = split ? d0 + half : d0 + 8;
   const T* src = (is_v ? V : K) + int64_t(r0 + (p0 - start)) * (is_v ? ldv : ldk) + int64_t(h) * D;
   const int64_t ld = is_v ? ldv : ldk;
   const int64_t blk = c.block(page, h);
   uint8_t* codes = (is_v ? c.vq : c.kq) + (blk << c.tshift) * D;
   float* sp = (is_v ? c.vs : c.ks) + blk;
-  Rope rot = rp;
-  if (is_v) rot.cos = nullptr;
 
-  // the new rows, NaN as 0; infinities keep their sign and saturate
-  float x[STEPS][8];
+  // the new rows (beyond the last, that one again), NaN as 0; infinities keep
+  // their sign and saturate
+  float x[STEPS][16];
   float m = 0.f;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    const int r = first + i * rstep;
-    if (r >= rows) break;
-    rotated8(src + int64_t(r) * ld, d, p0 + r, rot, x[i]);
+    const T* row = src + int64_t(min(first + i * rstep, rows - 1)) * ld;
+    float a[8] = {}, b8[8] = {};
+    if (i * rstep < rows) {
+      load8(row + d0, a);
+      load8(row + d1, b8);
+    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8; ++e) x[i][e] = a[e], x[i][8 + e] = b8[e];
+  }
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (i * rstep >= rows) break;
+      const int64_t at = int64_t(p0 + min(first + i * rstep, rows - 1)) * half + piece * 8;
+      float cs[8], sn[8];
+      load8(rp.cos + at, cs);
+      load8(rp.sin + at, sn);
+      // pair e: elements e and e + 8 of the piece, or 2 e and 2 e + 1
+      if (split) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn(x[i][e], x[i][8 + e], cs[e], sn[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn(x[i][2 * e], x[i][2 * e + 1], cs[e], sn[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
       const float a = fabsf(x[i][e]);
       if (a <= 3.4028234663852886e38f) {
         m = fmaxf(m, a);
@@ -80,7 +119,6 @@ __global__ void __launch_bounds__(512)
         if (a != a) x[i][e] = 0.f;
       }
     }
-  }
   const float old = slot0 ? *sp : 0.f;
   m = warp_max(m);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -116,9 +154,9 @@ __global__ void __launch_bounds__(512)
   for (int i = 0; i < STEPS; ++i) {
     const int r = first + i * rstep;
     if (r >= rows) break;
-    uint32_t o[2];
+    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -134,7 +172,9 @@ __global__ void __launch_bounds__(512)
         o[k] = a | (b << 16);
       }
     }
-    *reinterpret_cast<uint2*>(codes + int64_t(slot0 + r) * D + d) = make_uint2(o[0], o[1]);
+    uint8_t* dst = codes + int64_t(slot0 + r) * D;
+    *reinterpret_cast<uint2*>(dst + d0) = make_uint2(o[0], o[1]);
+    *reinterpret_cast<uint2*>(dst + d1) = make_uint2(o[2], o[3]);
   }
   if (bad) record_error(status, WQ_ERR_NONFINITE);
 }
