@@ -29,24 +29,30 @@ constexpr int BK = 128;
 // ---------------------------------------------------------------------------
 // Large products
 // ---------------------------------------------------------------------------
-constexpr int BM = 128, BN = 256;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
+// A pair of CTAs (one cluster) computes 256 tokens x 256 channels: each loads
+// 128 tokens and 128 channels, the products read both halves of the channels.
+// One CTA per 128 x 256 tile loads half as much again for the same products and
+// was held by L2 (9.6 TB/s) at 220 us for 4096 x 11008 x 4096.
+constexpr int BM = 128, BN = 256;  // per CTA: tokens; channels of the pair
+constexpr int STAGES = 6;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;
+constexpr int OUT_BYTES = 32 * 64 * 2;  // a warp's rows x 64 channels, on their way out
 // warps 0 to 3 copy and issue, 4 to 11 add: 168 registers a thread at launch,
 // split 56 to 224 (128 sums and two chunks of 32 on their way)
 constexpr int THREADS_L = 32 * (4 + EPI_WARPS);
 constexpr int REGS_ISSUE = 56, REGS_ADD = 224;
 static_assert(4 * REGS_ISSUE + EPI_WARPS * REGS_ADD <= (4 + EPI_WARPS) * 168, "registers");
-constexpr uint32_t IDESC_L = tc::idesc_e4m3_f32(BM, BN);
+constexpr uint32_t IDESC_L = tc::idesc_e4m3_f32(2 * BM, BN);
 
 struct SmemL {
   uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t SMEM_L = 1024 + size_t(STAGES) * STAGE_BYTES + sizeof(SmemL);
+constexpr size_t SMEM_L =
+    1024 + size_t(STAGES) * STAGE_BYTES + size_t(EPI_WARPS) * OUT_BYTES + sizeof(SmemL);
 
 // acc[0..1] += s * d[0..1] (two fp32 fused multiply-adds in one instruction)
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s2) {
@@ -74,9 +80,12 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  SmemL& sm = *reinterpret_cast<SmemL*>(tiles + size_t(STAGES) * STAGE_BYTES);
+  uint8_t* outs = tiles + size_t(STAGES) * STAGE_BYTES;
+  SmemL& sm = *reinterpret_cast<SmemL*>(outs + EPI_WARPS * OUT_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mtiles = (M + BM - 1) / BM, ntiles = (N + BN - 1) / BN;
+  const uint32_t rank = tc::cluster_rank();
+  const int pairs = int(gridDim.x) / 2, me = int(blockIdx.x) / 2;
+  const int mtiles = (M + 2 * BM - 1) / (2 * BM), ntiles = (N + BN - 1) / BN;
   const int total = mtiles * ntiles;
   const int kblocks = (K + BK - 1) / BK;
 
@@ -87,7 +96,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sm.tfull[b], 1);
-      tc::mbar_init(&sm.tempty[b], EPI_WARPS);
+      tc::mbar_init(&sm.tempty[b], 2 * EPI_WARPS);
     }
     tc::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -96,46 +105,52 @@ __global__ void __launch_bounds__(THREADS_L, 1)
     tc::tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tc::tmem_alloc(&sm.tmem_base, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(&sm.tmem_base, 512);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
   // the quantizer's codes and scales of X are complete from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------- producer
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = me; tile < total && ok; tile += pairs) {
         const int mt = tile % mtiles, nt = tile / mtiles;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
           if (!(ok = tc::wait_bounded(&sm.empty[s], ((it / STAGES) & 1u) ^ 1u, wd))) break;
           uint8_t* a = tiles + size_t(s) * STAGE_BYTES;
-          tc::mbar_arrive_expect_tx(&sm.full[s], STAGE_BYTES);
-          tc::tma_load_2d(a, &tmA, &sm.full[s], kb * BK, mt * BM);
-          tc::tma_load_2d(a + A_BYTES, &tmB, &sm.full[s], kb * BK, nt * BN);
+          // both CTAs' halves are counted by the leader's barrier
+          if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE_BYTES);
+          const uint32_t bar = tc::map_to(&sm.full[s], 0);
+          tc::tma_load_2d_pair(a, &tmA, bar, kb * BK, (mt * 2 + int(rank)) * BM);
+          tc::tma_load_2d_pair(a + A_BYTES, &tmB, bar, kb * BK, nt * BN + int(rank) * (BN / 2));
         }
       }
-      // the last load issued into each stage has landed before exit
-      const uint64_t dl = tc::globaltimer_ns() + tc::kDrainNs;
-      const uint32_t n = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint32_t i = it - 1 - j;
-        tc::wait_until(&sm.full[i % STAGES], (i / STAGES) & 1u, dl);
+      // the last load issued into each stage has landed before exit (the
+      // leader sees both CTAs', and the other one waits for it at the end)
+      if (rank == 0) {
+        const uint64_t dl = tc::globaltimer_ns() + tc::kDrainNs;
+        const uint32_t n = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
+        for (uint32_t j = 0; j < n; ++j) {
+          const uint32_t i = it - 1 - j;
+          tc::wait_until(&sm.full[i % STAGES], (i / STAGES) & 1u, dl);
+        }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ------------------------------------------------------ MMA issuer
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = me; tile < total && ok; tile += pairs) {
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t buf = it & 1u;
@@ -145,24 +160,27 @@ __global__ void __launch_bounds__(THREADS_L, 1)
           const uint32_t a = tc::smem_u32(tiles + size_t(s) * STAGE_BYTES), b = a + A_BYTES;
 #pragma unroll
           for (int k = 0; k < BK / 32; ++k)
-            tc::mma_f8_ss(tmem + buf * BN, tc::sdesc_k_sw128(a + k * 32),
-                          tc::sdesc_k_sw128(b + k * 32), IDESC_L, k != 0);
-          tc::mma_commit(&sm.empty[s]);
-          tc::mma_commit(&sm.tfull[buf]);
+            tc::mma_f8_ss_pair(tmem + buf * BN, tc::sdesc_k_sw128(a + k * 32),
+                               tc::sdesc_k_sw128(b + k * 32), IDESC_L, k != 0);
+          tc::mma_commit_pair(&sm.empty[s]);
+          tc::mma_commit_pair(&sm.tfull[buf]);
         }
       }
-      tc::mma_commit(&sm.drain);
+      tc::mma_commit_pair(&sm.drain);
       tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
-  } else if (warp >= 4) {
+  } else {
+    // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ADD));
-    const int q = warp & 3;           // tensor-memory lane quarter
+    const int q = warp & 3;            // tensor-memory lane quarter
     const int half = (warp - 4) >> 2;  // channels [128 half, 128 half + 128) of the tile
+    const uint32_t free0 = tc::map_to(&sm.tempty[0], 0), free1 = tc::map_to(&sm.tempty[1], 0);
+    const uint32_t out = tc::smem_u32(outs + (warp - 4) * OUT_BYTES);
     uint32_t it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    for (int tile = me; tile < total && ok; tile += pairs) {
       const int mt = tile % mtiles, nt = tile / mtiles;
-      const int row = mt * BM + q * 32 + lane;
+      const int row0 = (mt * 2 + int(rank)) * BM + q * 32, row = row0 + lane;
       const int n0 = nt * BN + half * 128;
       const float* sxp = sxT + (row < M ? row : M - 1);
       const float* swp = sw + int64_t(n0 < N ? n0 / 128 : 0) * kblocks;
@@ -170,54 +188,80 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      // scales two K blocks ahead
-      auto scale_at = [&](int kb) {
-        const int k = kb < kblocks ? kb : kblocks - 1;
-        return __ldg(sxp + k * ldsx) * __ldg(swp + k);
-      };
-      float s0 = scale_at(0), s1 = scale_at(1);
+      // scales two K blocks ahead (multiplied only when they are used)
+      auto next_k = [&](int kb) { return kb < kblocks ? kb : kblocks - 1; };
+      float x0 = __ldg(sxp), w0 = __ldg(swp);
+      float x1 = __ldg(sxp + next_k(1) * ldsx), w1 = __ldg(swp + next_k(1));
+      if (!(ok = tc::wait_warp(&sm.tfull[it & 1u], (it >> 1) & 1u, wd))) break;
+      tc::fence_after_sync();
+      // chunks of 32 channels, one on its way while the one before is added
+      uint32_t r[2][32];
+      tc::tmem_ld_x32(taddr + (it & 1u) * BN, r[0]);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        const uint64_t s2 = pair(s0, s0);
-        s0 = s1;
-        s1 = scale_at(kb + 2);
-        if (!(ok = tc::wait_warp(&sm.tfull[buf], (it >> 1) & 1u, wd))) break;
-        tc::fence_after_sync();
-        // a chunk of 32 channels is on its way while the one before is added
-        const uint32_t t = taddr + buf * BN;
-        uint32_t r[2][32];
-        tc::tmem_ld_x32(t, r[0]);
+        const float s = x0 * w0;
+        const uint64_t s2 = pair(s, s);
+        x0 = x1, w0 = w1;
+        x1 = __ldg(sxp + next_k(kb + 2) * ldsx);
+        w1 = __ldg(swp + next_k(kb + 2));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tc::tmem_wait_ld();
           if (c < 3) {
-            tc::tmem_ld_x32(t + (c + 1) * 32, r[(c + 1) & 1]);
+            tc::tmem_ld_x32(taddr + buf * BN + (c + 1) * 32, r[(c + 1) & 1]);
           } else {
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.tempty[buf]);
+            if (lane == 0) tc::mbar_arrive_at(buf ? free1 : free0);
+            if (kb + 1 < kblocks) {
+              if (!(ok = tc::wait_warp(&sm.tfull[buf ^ 1u], ((it + 1) >> 1) & 1u, wd))) break;
+              tc::fence_after_sync();
+              tc::tmem_ld_x32(taddr + (buf ^ 1u) * BN, r[0]);
+            }
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             fma2(acc[c * 16 + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], s2);
         }
+        if (!ok) break;
       }
-      if (ok && row < M) {
-        __nv_bfloat16* y = Y + int64_t(row) * N + n0;
+      if (!ok) break;
+      // 64 channels at a time through shared memory, so that a row's 128 bytes
+      // leave together
 #pragma unroll
-        for (int g = 0; g < 16; ++g)
-          if (n0 + g * 8 < N)
-            *reinterpret_cast<uint4*>(y + g * 8) =
-                make_uint4(bf16x2_of(acc[4 * g]), bf16x2_of(acc[4 * g + 1]),
-                           bf16x2_of(acc[4 * g + 2]), bf16x2_of(acc[4 * g + 3]));
+      for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const uint64_t* v = acc + h * 32 + 4 * g;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           out + lane * 128 + ((g ^ (lane & 7)) << 4)),
+                       "r"(bf16x2_of(v[0])), "r"(bf16x2_of(v[1])), "r"(bf16x2_of(v[2])),
+                       "r"(bf16x2_of(v[3]))
+                       : "memory");
+        }
+        __syncwarp();
+        const int col = n0 + h * 64 + (lane & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(out + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+          if (row0 + r < M && col < N) *reinterpret_cast<uint4*>(Y + int64_t(row0 + r) * N + col) = v;
+        }
       }
     }
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  // neither CTA leaves while the other may reach its memory
+  tc::cluster_sync();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -523,18 +567,42 @@ cudaError_t set_smem(Kern kern, size_t bytes, int which) {
 
 struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  Launch(int grid, int threads, size_t smem, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  Launch(int grid, int threads, size_t smem, cudaStream_t s, int cluster = 1) {
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
   }
 };
+
+// CTA pairs of the large product that are on the device at a time.
+int max_pairs() {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && known[dev]) return known[dev];
+  Launch l(2 * (sm_count() / 2), wq::fp8b::THREADS_L, wq::fp8b::SMEM_L, nullptr, 2);
+  l.cfg.attrs = l.attr + 1;
+  l.cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, wq::fp8b::gemm_fp8_block_kernel, &l.cfg) != cudaSuccess)
+    n = 0;
+  (void)cudaGetLastError();
+  if (n < 1) n = 1;
+  if (n > sm_count() / 2) n = sm_count() / 2;
+  if (dev < 64) known[dev] = n;
+  return n;
+}
 
 template <int NT>
 int launch_split(const CUtensorMap& tx, const void* Wq, const float* sx, const float* sw,
@@ -582,14 +650,14 @@ int launch_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, c
     case 128: return launch_split<128>(tx, Wq, sx, sw, p, M, N, K, Y, w, s);
   }
   CUtensorMap tw;
-  st = make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(N), uint64_t(K), BN, BK,
+  st = make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(N), uint64_t(K), BN / 2, BK,
                     128);
   if (st != WQ_OK) return st;
   WQ_CUDA_CHECK(set_smem(gemm_fp8_block_kernel, SMEM_L, 0));
-  const int64_t total = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-  if (total > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
-  const int grid = int(total < sm_count() ? total : sm_count());
-  Launch l(grid, THREADS_L, SMEM_L, s);
+  const int64_t total = ((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN);
+  if (total > 0x3fffffff) return WQ_ERR_UNSUPPORTED;
+  const int pairs = int(total < max_pairs() ? total : max_pairs());
+  Launch l(2 * pairs, THREADS_L, SMEM_L, s, 2);
   WQ_CUDA_CHECK(cudaLaunchKernelEx(&l.cfg, gemm_fp8_block_kernel, tx, tw, sx, p.mp, sw,
                                    static_cast<__nv_bfloat16*>(Y), int(M), int(N), int(K),
                                    status_ptr(), wait_limit_ns()));
