@@ -29,22 +29,25 @@ constexpr int BK = 128;
 // ---------------------------------------------------------------------------
 // Large products
 // ---------------------------------------------------------------------------
-// A pair of CTAs (one cluster) computes 256 tokens x 256 channels: each loads
-// 128 tokens and 128 channels, the products read both halves of the channels.
-// One CTA per 128 x 256 tile loads half as much again for the same products and
-// was held by L2 (9.6 TB/s) at 220 us for 4096 x 11008 x 4096.
-constexpr int BM = 128, BN = 256;  // per CTA: tokens; channels of the pair
-constexpr int STAGES = 6;
-constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;
+// 4 x 48 KB of operands on their way, two 128 x 256 sums in tensor memory.  At
+// 4096 x 11008 x 4096 the copies and products alone take 117 us (3.2 PFLOP/s);
+// with the sums read back for every K block the GPU is at its 1 kW cap (1.63
+// GHz) and at 180 us: what is left is the hand-off of two buffers, not L2 (a
+// CTA pair on 256 x 256 tiles, a third less traffic, measured the same), nor
+// the additions (without them 175 us), nor more and smaller buffers (four of
+// 128 channels: 220 us, operands are read twice).
+constexpr int BM = 128, BN = 256;
+constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int EPI_WARPS = 8;
-constexpr int OUT_BYTES = 32 * 64 * 2;  // a warp's rows x 64 channels, on their way out
-// warps 0 to 3 copy and issue, 4 to 11 add: 168 registers a thread at launch,
-// split 56 to 224 (128 sums and two chunks of 32 on their way)
+constexpr int EPI_WARPS = 16;
+constexpr int OUT_BYTES = 32 * 32 * 2;  // a warp's rows x 32 channels, on their way out
+// warps 0 to 3 copy and issue, 4 to 19 add: 96 registers a thread at launch,
+// split 32 to 112 (64 sums and a chunk of 32 on its way)
 constexpr int THREADS_L = 32 * (4 + EPI_WARPS);
-constexpr int REGS_ISSUE = 56, REGS_ADD = 224;
-static_assert(4 * REGS_ISSUE + EPI_WARPS * REGS_ADD <= (4 + EPI_WARPS) * 168, "registers");
-constexpr uint32_t IDESC_L = tc::idesc_e4m3_f32(2 * BM, BN);
+constexpr int REGS_ISSUE = 32, REGS_ADD = 112;
+static_assert(4 * REGS_ISSUE + EPI_WARPS * REGS_ADD <= (4 + EPI_WARPS) * 96, "registers");
+constexpr uint32_t IDESC_L = tc::idesc_e4m3_f32(BM, BN);
 
 struct SmemL {
   uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], drain;
@@ -83,9 +86,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   uint8_t* outs = tiles + size_t(STAGES) * STAGE_BYTES;
   SmemL& sm = *reinterpret_cast<SmemL*>(outs + EPI_WARPS * OUT_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = tc::cluster_rank();
-  const int pairs = int(gridDim.x) / 2, me = int(blockIdx.x) / 2;
-  const int mtiles = (M + 2 * BM - 1) / (2 * BM), ntiles = (N + BN - 1) / BN;
+  const int mtiles = (M + BM - 1) / BM, ntiles = (N + BN - 1) / BN;
   const int total = mtiles * ntiles;
   const int kblocks = (K + BK - 1) / BK;
 
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sm.tfull[b], 1);
-      tc::mbar_init(&sm.tempty[b], 2 * EPI_WARPS);
+      tc::mbar_init(&sm.tempty[b], EPI_WARPS);
     }
     tc::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -105,12 +106,11 @@ __global__ void __launch_bounds__(THREADS_L, 1)
     tc::tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
-    tc::tmem_alloc_pair(&sm.tmem_base, 512);
-    tc::tmem_relinquish_pair();
+    tc::tmem_alloc(&sm.tmem_base, 512);
+    tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
@@ -123,132 +123,124 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       // -------------------------------------------------------- producer
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = me; tile < total && ok; tile += pairs) {
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         const int mt = tile % mtiles, nt = tile / mtiles;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
           if (!(ok = tc::wait_bounded(&sm.empty[s], ((it / STAGES) & 1u) ^ 1u, wd))) break;
           uint8_t* a = tiles + size_t(s) * STAGE_BYTES;
-          // both CTAs' halves are counted by the leader's barrier
-          if (rank == 0) tc::mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE_BYTES);
-          const uint32_t bar = tc::map_to(&sm.full[s], 0);
-          tc::tma_load_2d_pair(a, &tmA, bar, kb * BK, (mt * 2 + int(rank)) * BM);
-          tc::tma_load_2d_pair(a + A_BYTES, &tmB, bar, kb * BK, nt * BN + int(rank) * (BN / 2));
+          tc::mbar_arrive_expect_tx(&sm.full[s], STAGE_BYTES);
+          tc::tma_load_2d(a, &tmA, &sm.full[s], kb * BK, mt * BM);
+          tc::tma_load_2d(a + A_BYTES, &tmB, &sm.full[s], kb * BK, nt * BN);
         }
       }
-      // the last load issued into each stage has landed before exit (the
-      // leader sees both CTAs', and the other one waits for it at the end)
-      if (rank == 0) {
-        const uint64_t dl = tc::globaltimer_ns() + tc::kDrainNs;
-        const uint32_t n = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
-        for (uint32_t j = 0; j < n; ++j) {
-          const uint32_t i = it - 1 - j;
-          tc::wait_until(&sm.full[i % STAGES], (i / STAGES) & 1u, dl);
-        }
+      // the last load issued into each stage has landed before exit
+      const uint64_t dl = tc::globaltimer_ns() + tc::kDrainNs;
+      const uint32_t n = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint32_t i = it - 1 - j;
+        tc::wait_until(&sm.full[i % STAGES], (i / STAGES) & 1u, dl);
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------ MMA issuer
+      // (the whole warp walks the loop and one lane issues, so that operand
+      // addresses stay in uniform registers)
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = me; tile < total && ok; tile += pairs) {
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t buf = it & 1u;
-          if (!(ok = tc::wait_bounded(&sm.tempty[buf], ((it >> 1) & 1u) ^ 1u, wd))) break;
-          if (!(ok = tc::wait_bounded(&sm.full[s], (it / STAGES) & 1u, wd))) break;
+          if (!(ok = tc::wait_warp(&sm.full[s], (it / STAGES) & 1u, wd))) break;
+          if (!(ok = tc::wait_warp(&sm.tempty[buf], ((it >> 1) & 1u) ^ 1u, wd))) break;
           tc::fence_after_sync();
-          const uint32_t a = tc::smem_u32(tiles + size_t(s) * STAGE_BYTES), b = a + A_BYTES;
+          const uint32_t a = tc::smem_u32(tiles) + uint32_t(s) * STAGE_BYTES, b = a + A_BYTES;
+          const uint64_t da = tc::sdesc_k_sw128(a), db = tc::sdesc_k_sw128(b);
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            tc::mma_f8_ss_pair(tmem + buf * BN, tc::sdesc_k_sw128(a + k * 32),
-                               tc::sdesc_k_sw128(b + k * 32), IDESC_L, k != 0);
-          tc::mma_commit_pair(&sm.empty[s]);
-          tc::mma_commit_pair(&sm.tfull[buf]);
+            for (int k = 0; k < BK / 32; ++k)
+              tc::mma_f8_ss(tmem + buf * BN, da + uint64_t(k * 2), db + uint64_t(k * 2), IDESC_L,
+                            k != 0);
+            tc::mma_commit(&sm.empty[s]);
+            tc::mma_commit(&sm.tfull[buf]);
+          }
+          __syncwarp();
         }
       }
-      tc::mma_commit_pair(&sm.drain);
-      tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
+      if (tc::elect_one()) {
+        tc::mma_commit(&sm.drain);
+        tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ADD));
     const int q = warp & 3;            // tensor-memory lane quarter
-    const int half = (warp - 4) >> 2;  // channels [128 half, 128 half + 128) of the tile
-    const uint32_t free0 = tc::map_to(&sm.tempty[0], 0), free1 = tc::map_to(&sm.tempty[1], 0);
+    const int part = (warp - 4) >> 2;  // channels [64 part, 64 part + 64) of the tile
     const uint32_t out = tc::smem_u32(outs + (warp - 4) * OUT_BYTES);
     uint32_t it = 0;
     bool ok = true;
-    for (int tile = me; tile < total && ok; tile += pairs) {
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       const int mt = tile % mtiles, nt = tile / mtiles;
-      const int row0 = (mt * 2 + int(rank)) * BM + q * 32, row = row0 + lane;
-      const int n0 = nt * BN + half * 128;
-      const float* sxp = sxT + (row < M ? row : M - 1);
+      const int row0 = mt * BM + q * 32;
+      const int n0 = nt * BN + part * 64;
+      const float* sxp = sxT + (row0 + lane < M ? row0 + lane : M - 1);
       const float* swp = sw + int64_t(n0 < N ? n0 / 128 : 0) * kblocks;
-      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(half) * 128;
-      uint64_t acc[64];
+      const uint32_t taddr = tmem + (uint32_t(q * 32) << 16) + uint32_t(part) * 64;
+      uint64_t acc[32];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0;
-      // scales two K blocks ahead (multiplied only when they are used)
-      auto next_k = [&](int kb) { return kb < kblocks ? kb : kblocks - 1; };
-      float x0 = __ldg(sxp), w0 = __ldg(swp);
-      float x1 = __ldg(sxp + next_k(1) * ldsx), w1 = __ldg(swp + next_k(1));
-      if (!(ok = tc::wait_warp(&sm.tfull[it & 1u], (it >> 1) & 1u, wd))) break;
-      tc::fence_after_sync();
-      // chunks of 32 channels, one on its way while the one before is added
-      uint32_t r[2][32];
-      tc::tmem_ld_x32(taddr + (it & 1u) * BN, r[0]);
+      for (int j = 0; j < 32; ++j) acc[j] = 0;
+      // scales one K block ahead (multiplied only when they are used)
+      float x1 = __ldg(sxp), w1 = __ldg(swp);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        const float s = x0 * w0;
+        const float s = x1 * w1;
         const uint64_t s2 = pair(s, s);
-        x0 = x1, w0 = w1;
-        x1 = __ldg(sxp + next_k(kb + 2) * ldsx);
-        w1 = __ldg(swp + next_k(kb + 2));
+        if (kb + 1 < kblocks) {
+          sxp += ldsx;
+          ++swp;
+        }
+        x1 = __ldg(sxp), w1 = __ldg(swp);
+        if (!(ok = tc::wait_warp(&sm.tfull[buf], (it >> 1) & 1u, wd))) break;
+        tc::fence_after_sync();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tc::tmem_ld_x32(taddr + buf * BN + c * 32, r);
           tc::tmem_wait_ld();
-          if (c < 3) {
-            tc::tmem_ld_x32(taddr + buf * BN + (c + 1) * 32, r[(c + 1) & 1]);
-          } else {
+          if (c == 1) {
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_at(buf ? free1 : free0);
-            if (kb + 1 < kblocks) {
-              if (!(ok = tc::wait_warp(&sm.tfull[buf ^ 1u], ((it + 1) >> 1) & 1u, wd))) break;
-              tc::fence_after_sync();
-              tc::tmem_ld_x32(taddr + (buf ^ 1u) * BN, r[0]);
-            }
+            if (lane == 0) tc::mbar_arrive_relaxed(&sm.tempty[buf]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            fma2(acc[c * 16 + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], s2);
+          for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], r[2 * j], r[2 * j + 1], s2);
         }
-        if (!ok) break;
       }
       if (!ok) break;
-      // 64 channels at a time through shared memory, so that a row's 128 bytes
+      // 32 channels at a time through shared memory, so that 64 bytes of a row
       // leave together
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const uint64_t* v = acc + h * 32 + 4 * g;
+        for (int g = 0; g < 4; ++g) {
+          const uint64_t* v = acc + h * 16 + 4 * g;
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           out + lane * 128 + ((g ^ (lane & 7)) << 4)),
+                           out + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
                        "r"(bf16x2_of(v[0])), "r"(bf16x2_of(v[1])), "r"(bf16x2_of(v[2])),
                        "r"(bf16x2_of(v[3]))
                        : "memory");
         }
         __syncwarp();
-        const int col = n0 + h * 64 + (lane & 7) * 8;
+        const int col = n0 + h * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2);
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(out + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+                       : "r"(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
           if (row0 + r < M && col < N) *reinterpret_cast<uint4*>(Y + int64_t(row0 + r) * N + col) = v;
         }
       }
@@ -257,11 +249,9 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  // neither CTA leaves while the other may reach its memory
-  tc::cluster_sync();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc_pair(tmem, 512);
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -372,11 +362,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
           tc::tma_load_2d(w, &tmW, &sm.full[s], kb * BK, nt * 128);
         }
         tc::tma_load_2d(w + P::W_BYTES, &tmX, &sm.full[s], kb * BK, mt * NT);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-            "[%3];" ::"r"(tc::smem_u32(sscale + s * NT)),
-            "l"(sxT + kb * ldsx + int64_t(mt) * NT), "r"(P::S_BYTES), "r"(tc::smem_u32(&sm.full[s]))
-            : "memory");
+        tc::bulk_load(sscale + s * NT, sxT + kb * ldsx + int64_t(mt) * NT, P::S_BYTES, &sm.full[s]);
         if (++kb == kblocks) kb = 0, ++tile;
       }
       const uint64_t dl = tc::globaltimer_ns() + tc::kDrainNs;
@@ -567,42 +553,18 @@ cudaError_t set_smem(Kern kern, size_t bytes, int which) {
 
 struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  Launch(int grid, int threads, size_t smem, cudaStream_t s, int cluster = 1) {
+  cudaLaunchAttribute attr[1];
+  Launch(int grid, int threads, size_t smem, cudaStream_t s) {
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
   }
 };
-
-// CTA pairs of the large product that are on the device at a time.
-int max_pairs() {
-  static std::mutex mu;
-  static int known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 64 && known[dev]) return known[dev];
-  Launch l(2 * (sm_count() / 2), wq::fp8b::THREADS_L, wq::fp8b::SMEM_L, nullptr, 2);
-  l.cfg.attrs = l.attr + 1;
-  l.cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, wq::fp8b::gemm_fp8_block_kernel, &l.cfg) != cudaSuccess)
-    n = 0;
-  (void)cudaGetLastError();
-  if (n < 1) n = 1;
-  if (n > sm_count() / 2) n = sm_count() / 2;
-  if (dev < 64) known[dev] = n;
-  return n;
-}
 
 template <int NT>
 int launch_split(const CUtensorMap& tx, const void* Wq, const float* sx, const float* sw,
@@ -650,14 +612,14 @@ int launch_gemm_fp8_block(const void* X, int64_t M, int64_t K, const void* Wq, c
     case 128: return launch_split<128>(tx, Wq, sx, sw, p, M, N, K, Y, w, s);
   }
   CUtensorMap tw;
-  st = make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(N), uint64_t(K), BN / 2, BK,
+  st = make_tmap_2d(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, uint64_t(N), uint64_t(K), BN, BK,
                     128);
   if (st != WQ_OK) return st;
   WQ_CUDA_CHECK(set_smem(gemm_fp8_block_kernel, SMEM_L, 0));
-  const int64_t total = ((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN);
-  if (total > 0x3fffffff) return WQ_ERR_UNSUPPORTED;
-  const int pairs = int(total < max_pairs() ? total : max_pairs());
-  Launch l(2 * pairs, THREADS_L, SMEM_L, s, 2);
+  const int64_t total = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+  if (total > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
+  const int grid = int(total < sm_count() ? total : sm_count());
+  Launch l(grid, THREADS_L, SMEM_L, s);
   WQ_CUDA_CHECK(cudaLaunchKernelEx(&l.cfg, gemm_fp8_block_kernel, tx, tw, sx, p.mp, sw,
                                    static_cast<__nv_bfloat16*>(Y), int(M), int(N), int(K),
                                    status_ptr(), wait_limit_ns()));
