@@ -272,9 +272,9 @@ struct Split {
   static constexpr int BUFS = 4;
   static constexpr uint32_t TMEM = NT * BUFS < 32 ? 32 : NT * BUFS;
   struct Bars {
-    uint64_t full[STAGES], empty[STAGES], tfull[BUFS], tempty[BUFS], parts, told, drain;
+    uint64_t full[STAGES], empty[STAGES], tfull[BUFS], tempty[BUFS], drain;
     uint32_t tmem_base;
-    int abort_flag, last;
+    int abort_flag;
   };
   static constexpr size_t SMEM = 1024 + size_t(STAGES) * (STAGE + S_BYTES) + sizeof(Bars);
 };
@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
   const int64_t U = int64_t(ntiles) * mtiles * kblocks, G = gridDim.x;
   const int64_t u0 = first_unit(blockIdx.x, U, G), u1 = first_unit(blockIdx.x + 1, U, G);
 
+  const int n_units = int(u1 - u0), pre = n_units < P::STAGES ? n_units : P::STAGES;
+  const int kb0 = int(u0 % kblocks), tile0 = int(u0 / kblocks);
   if (threadIdx.x == 0) {
     for (int s = 0; s < P::STAGES; ++s) {
       tc::mbar_init(&sm.full[s], 1);
@@ -317,13 +319,17 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
       tc::mbar_init(&sm.tfull[b], 1);
       tc::mbar_init(&sm.tempty[b], P::EWARPS);
     }
-    tc::mbar_init(&sm.parts, P::EWARPS);
-    tc::mbar_init(&sm.told, 1);
     tc::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     tc::fence_mbar_init();
-    tc::tma_prefetch_desc(&tmW);
-    tc::tma_prefetch_desc(&tmX);
+    // W does not depend on the kernel before this one (the quantizer of X): a
+    // ring's worth of weight tiles is requested before anything else is set up
+    int kb = kb0, tile = tile0;
+    for (int i = 0; i < pre; ++i) {
+      tc::mbar_arrive_expect_tx(&sm.full[i], P::STAGE + P::S_BYTES);
+      tc::tma_load_2d(tiles + size_t(i) * P::STAGE, &tmW, &sm.full[i], kb * BK, tile / mtiles * 128);
+      if (++kb == kblocks) kb = 0, ++tile;
+    }
   }
   if (warp == 1) {
     tc::tmem_alloc(&sm.tmem_base, P::TMEM);
@@ -337,22 +343,10 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // W does not depend on the kernel before this one (the quantizer of X):
-      // a ring's worth of weight tiles is requested before it has completed
-      const int n = int(u1 - u0);
-      const int pre = n < P::STAGES ? n : P::STAGES;
-      const int kb0 = int(u0 % kblocks), tile0 = int(u0 / kblocks);
-      int kb = kb0, tile = tile0;
-      for (int i = 0; i < pre; ++i) {
-        tc::mbar_arrive_expect_tx(&sm.full[i], P::STAGE + P::S_BYTES);
-        tc::tma_load_2d(tiles + size_t(i) * P::STAGE, &tmW, &sm.full[i], kb * BK,
-                        tile / mtiles * 128);
-        if (++kb == kblocks) kb = 0, ++tile;
-      }
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      kb = kb0, tile = tile0;
+      int kb = kb0, tile = tile0;
       int it = 0;
-      for (; it < n; ++it) {
+      for (; it < n_units; ++it) {
         const int s = it % P::STAGES;
         const int mt = tile % mtiles, nt = tile / mtiles;
         uint8_t* w = tiles + size_t(s) * P::STAGE;
@@ -375,8 +369,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = tc::idesc_e4m3_f32(128, NT);
-      const int n = int(u1 - u0);
-      for (int it = 0; it < n; ++it) {
+      for (int it = 0; it < n_units; ++it) {
         const int s = it % P::STAGES;
         const uint32_t buf = uint32_t(it) % P::BUFS;
         if (!tc::wait_bounded(&sm.tempty[buf], ((it / P::BUFS) & 1u) ^ 1u, wd)) break;
@@ -397,10 +390,8 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
     const int q = warp & 3;
     const int cg = (warp - 2) >> 2;           // token group of COLS
     const int ch = q * 32 + lane;             // channel within the tile
-    const int et = threadIdx.x - 64;          // epilogue thread
     int it = 0;
     int slot = 0;
-    uint32_t cuts = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
       const int tile = int(u / kblocks);
@@ -408,17 +399,24 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
       const int64_t e = u1 < t1 ? u1 : t1;
       const int mt = tile % mtiles, nt = tile / mtiles;
       const int n = nt * 128 + ch;
+      // weight scales: lane i holds that of the segment's K block 32 b + i, and
+      // the next 32 are on their way
       const float* swp = sw + int64_t(nt) * kblocks + (u - t0);
+      const int blocks = int(e - u);
+      float w_now = lane < blocks ? __ldg(swp + lane) : 0.f;
+      float w_next = lane + 32 < blocks ? __ldg(swp + lane + 32) : 0.f;
       const bool whole = u == t0 && e == t1;
       float acc[P::COLS];
 #pragma unroll
       for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
-      float w = __ldg(swp);
-      for (; u < e; ++u, ++it) {
+      for (int i = 0; i < blocks; ++i, ++u, ++it) {
         const uint32_t buf = uint32_t(it) % P::BUFS;
         const int s = it % P::STAGES;
-        const float wk = w;
-        if (u + 1 < e) w = __ldg(++swp);
+        const float wk = __shfl_sync(0xffffffffu, w_now, i & 31);
+        if ((i & 31) == 31) {
+          w_now = w_next;
+          w_next = i + 33 + lane < blocks ? __ldg(swp + i + 33 + lane) : 0.f;
+        }
         // both, so that the scales (written by the copy) are seen as well
         if (!(ok = tc::wait_warp(&sm.full[s], (it / P::STAGES) & 1u, wd))) break;
         if (!(ok = tc::wait_warp(&sm.tfull[buf], (it / P::BUFS) & 1u, wd))) break;
@@ -446,35 +444,32 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         // the stage is free when every epilogue warp has read its scales and
         // the tensor cores its tiles (they have: tfull)
         if (lane == 0) {
-          tc::mbar_arrive(&sm.tempty[buf]);
-          tc::mbar_arrive(&sm.empty[s]);
+          tc::mbar_arrive_relaxed(&sm.tempty[buf]);
+          tc::mbar_arrive_relaxed(&sm.empty[s]);
         }
       }
       if (!ok) break;
       const int tok0 = mt * NT + cg * P::COLS;
       if (!whole) {
-        // a cut tile: this CTA's part goes to the workspace, and the last of
-        // the tile's CTAs adds the parts in K order
+        // a cut tile: this warp's part (32 channels) goes to the workspace, and
+        // the last of the tile's warps for these channels adds the parts in K
+        // order.  The counter's release and acquire cover the warp's stores and
+        // loads (ordered with its lane 0 by the warp's synchronisation).
         const int64_t part = int64_t(P::COLS) * 128 * (NT / P::COLS);
         float* dst = partials + (int64_t(blockIdx.x) * 2 + slot) * part + cg * P::COLS * 128 + ch;
         slot = 1;
 #pragma unroll
-        for (int j = 0; j < P::COLS; ++j) __stcg(dst + j * 128, acc[j]);
-        __threadfence();
+        for (int j = 0; j < P::COLS; ++j)
+          if (tok0 + j < M) __stcg(dst + j * 128, acc[j]);
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.parts);
         const int c0 = owner(t0, U, G), c1 = owner(t1 - 1, U, G);
-        if (et < 32) {
-          if (!(ok = tc::wait_warp(&sm.parts, cuts & 1u, wd))) break;
-          if (lane == 0) {
-            sm.last = atomicAdd(counters + tile, 1) == c1 - c0;
-            tc::mbar_arrive(&sm.told);
-          }
-        }
-        if (!(ok = tc::wait_warp(&sm.told, cuts & 1u, wd))) break;
-        ++cuts;
-        if (!sm.last) continue;
-        __threadfence();
+        int before = 0;
+        if (lane == 0)
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(counters + int64_t(tile) * P::EWARPS + (warp - 2))
+                       : "memory");
+        if (__shfl_sync(0xffffffffu, before, 0) != c1 - c0) continue;
 #pragma unroll
         for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
         for (int c = c0; c <= c1; ++c) {
@@ -483,7 +478,8 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
           const bool second = first_unit(c, U, G) < t0 && (first_unit(c, U, G) % kblocks) != 0;
           const float* src = partials + (int64_t(c) * 2 + second) * part + cg * P::COLS * 128 + ch;
 #pragma unroll
-          for (int j = 0; j < P::COLS; ++j) acc[j] += __ldcg(src + j * 128);
+          for (int j = 0; j < P::COLS; ++j)
+            if (tok0 + j < M) acc[j] += __ldcg(src + j * 128);
         }
       }
       if (n < N) {
@@ -520,7 +516,7 @@ int split_tokens(int64_t M, int64_t N) {
 struct Plan {
   int nt;
   int64_t mp;                  // tokens, padded to a multiple of 128
-  int n_counters;
+  int tiles, n_counters;
   size_t sx, counters, partials, bytes;  // offsets in the workspace, and its size
 };
 
@@ -531,7 +527,8 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
   p.mp = (M + 127) / 128 * 128;
   p.sx = up256(size_t(M) * size_t(K));
   p.counters = p.sx + up256(size_t(kb * p.mp) * 4);
-  p.n_counters = p.nt ? int(((N + 127) / 128) * ((M + p.nt - 1) / p.nt)) : 0;
+  p.tiles = p.nt ? int(((N + 127) / 128) * ((M + p.nt - 1) / p.nt)) : 0;
+  p.n_counters = p.tiles * (p.nt > 64 ? 8 : 4);  // one for each adding warp
   p.partials = p.counters + up256(size_t(p.n_counters) * 4);
   p.bytes = p.partials + (p.nt ? size_t(sm_count()) * 2 * p.nt * 128 * 4 : 0);
   return p;
@@ -577,7 +574,7 @@ int launch_split(const CUtensorMap& tx, const void* Wq, const float* sx, const f
   if (st != WQ_OK) return st;
   constexpr int which = NT == 16 ? 1 : NT == 32 ? 2 : NT == 64 ? 3 : 4;
   WQ_CUDA_CHECK(set_smem(gemm_fp8_block_split_kernel<NT>, Split<NT>::SMEM, which));
-  const int64_t units = int64_t(p.n_counters) * ((K + 127) / 128);
+  const int64_t units = int64_t(p.tiles) * ((K + 127) / 128);
   const int grid = int(units < sm_count() ? units : sm_count());
   Launch l(grid, Split<NT>::THREADS, Split<NT>::SMEM, s);
   WQ_CUDA_CHECK(cudaLaunchKernelEx(&l.cfg, gemm_fp8_block_split_kernel<NT>, tw, tx, sx, p.mp, sw,

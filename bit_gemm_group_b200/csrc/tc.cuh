@@ -51,8 +51,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// For what a warp has read from tensor memory (complete: tmem_wait_ld) and
-// nothing else: relaxed, since a release first waits for the warp's global
+// For what a warp has read (from tensor memory: complete after tmem_wait_ld; from
+// shared memory: values in use) and nothing that it wrote: relaxed, since a release first waits for the warp's global
 // loads on their way (900 cycles of a K block's 1500 in the large block-scaled
 // product).
 __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
