@@ -68,6 +68,9 @@ __device__ __forceinline__ uint64_t pair(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
   return r;
 }
+__device__ __forceinline__ float one_of(uint64_t v, int i) {
+  return __uint_as_float(uint32_t(i ? v >> 32 : v));
+}
 __device__ __forceinline__ uint32_t bf16x2_of(uint64_t v) {
   uint32_t a, b;
   asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
@@ -406,9 +409,9 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
       float w_now = lane < blocks ? __ldg(swp + lane) : 0.f;
       float w_next = lane + 32 < blocks ? __ldg(swp + lane + 32) : 0.f;
       const bool whole = u == t0 && e == t1;
-      float acc[P::COLS];
+      uint64_t acc[P::COLS / 2];
 #pragma unroll
-      for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
+      for (int j = 0; j < P::COLS / 2; ++j) acc[j] = 0;
       for (int i = 0; i < blocks; ++i, ++u, ++it) {
         const uint32_t buf = uint32_t(it) % P::BUFS;
         const int s = it % P::STAGES;
@@ -423,20 +426,28 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         tc::fence_after_sync();
         const uint32_t taddr =
             tmem + (uint32_t(q * 32) << 16) + buf * NT + uint32_t(cg) * P::COLS;
-        const float4* sp = reinterpret_cast<const float4*>(sscale + s * NT + cg * P::COLS);
+        const uint32_t sp = tc::smem_u32(sscale + s * NT + cg * P::COLS);
+        const uint64_t w2 = pair(wk, wk);
+        constexpr int CH = P::COLS > 32 ? 32 : P::COLS;  // tokens read back at a time
 #pragma unroll
-        for (int c = 0; c < P::COLS / 16; ++c) {
-          uint32_t r[16];
-          tc::tmem_ld_x16(taddr + c * 16, r);
+        for (int c = 0; c < P::COLS / CH; ++c) {
+          uint32_t r[CH];
+          if constexpr (CH == 32)
+            tc::tmem_ld_x32(taddr + c * CH, r);
+          else
+            tc::tmem_ld_x16(taddr + c * CH, r);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 f = sp[c * 4 + j];
-            float* a = acc + c * 16 + j * 4;
-            a[0] = fmaf(__uint_as_float(r[4 * j]) * wk, f.x, a[0]);
-            a[1] = fmaf(__uint_as_float(r[4 * j + 1]) * wk, f.y, a[1]);
-            a[2] = fmaf(__uint_as_float(r[4 * j + 2]) * wk, f.z, a[2]);
-            a[3] = fmaf(__uint_as_float(r[4 * j + 3]) * wk, f.w, a[3]);
+          for (int j = 0; j < CH / 4; ++j) {
+            uint64_t f[2];
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                         : "=l"(f[0]), "=l"(f[1])
+                         : "r"(sp + (c * CH + j * 4) * 4));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(f[k]) : "l"(w2));
+              fma2(acc[(c * CH + j * 4) / 2 + k], r[j * 4 + 2 * k], r[j * 4 + 2 * k + 1], f[k]);
+            }
           }
         }
         tc::fence_before_sync();
@@ -460,7 +471,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         slot = 1;
 #pragma unroll
         for (int j = 0; j < P::COLS; ++j)
-          if (tok0 + j < M) __stcg(dst + j * 128, acc[j]);
+          if (tok0 + j < M) __stcg(dst + j * 128, one_of(acc[j / 2], j & 1));
         __syncwarp();
         const int c0 = owner(t0, U, G), c1 = owner(t1 - 1, U, G);
         int before = 0;
@@ -471,21 +482,23 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
                        : "memory");
         if (__shfl_sync(0xffffffffu, before, 0) != c1 - c0) continue;
 #pragma unroll
-        for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
+        for (int j = 0; j < P::COLS / 2; ++j) acc[j] = 0;
         for (int c = c0; c <= c1; ++c) {
           // a CTA's first part is in slot 0; it is a second one when the CTA
           // began with the tail of an earlier tile
           const bool second = first_unit(c, U, G) < t0 && (first_unit(c, U, G) % kblocks) != 0;
           const float* src = partials + (int64_t(c) * 2 + second) * part + cg * P::COLS * 128 + ch;
 #pragma unroll
-          for (int j = 0; j < P::COLS; ++j)
-            if (tok0 + j < M) acc[j] += __ldcg(src + j * 128);
+          for (int j = 0; j < P::COLS / 2; ++j) {  // (all loads in flight)
+            const uint64_t v = pair(__ldcg(src + 2 * j * 128), __ldcg(src + (2 * j + 1) * 128));
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc[j]) : "l"(v));
+          }
         }
       }
       if (n < N) {
 #pragma unroll
         for (int j = 0; j < P::COLS; ++j)
-          if (tok0 + j < M) Y[int64_t(tok0 + j) * N + n] = __float2bfloat16_rn(acc[j]);
+          if (tok0 + j < M) Y[int64_t(tok0 + j) * N + n] = __float2bfloat16_rn(one_of(acc[j / 2], j & 1));
       }
     }
   }
