@@ -177,7 +177,7 @@ struct Args {
   float scale_log2;
   float* parts;      // [2 W][RB][D]
   float* part_ml;    // [2 W][RB][2]
-  int64_t* prefix;   // [B + 1] first unit of each sequence
+  Cut* cuts;         // [W] the segments that the runs' starts cut
 };
 
 template <typename TQ, int FMT, int D>
@@ -230,10 +230,6 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
             start_at[w] = u - first;
           }
         }
-        if (blockIdx.x == 0 && s.b < bt.B) {
-          ar.prefix[s.b] = first;
-          if (s.b == bt.B - 1) ar.prefix[bt.B] = U;
-        }
       }
       __syncthreads();
     }
@@ -244,15 +240,14 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
       run_at[threadIdx.x] = id < W ? run_start(id, U, W) : -1;
     }
     __syncthreads();
-    if (U == 0 && pass == 0) {
-      if (blockIdx.x == 0)
-        for (int b = int(threadIdx.x); b <= bt.B; b += WARPS * 32) ar.prefix[b] = 0;
-      return;
-    }
+    if (U == 0) break;
   }
   const int64_t W = workers(U, int64_t(gridDim.x) * WARPS);
   const int64_t id = int64_t(warp) * gridDim.x + blockIdx.x;
-  if (id >= W) return;
+  if (id >= W) {
+    if (lane == 0) write_cut(ar.cuts + id, false, 0, 0, 0, 0, 0, 0, 0, 0, 0);
+    return;
+  }
   u0 = run_start(id, U, W);
   u1 = run_start(id + 1, U, W);
   me.b = start_b[warp];
@@ -264,6 +259,9 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     if (me.tile < 0) me.tile = 0, me.at = 1;  // the run begins with the segment's own unit
     me.rb = int(seg % me.nrb);
     me.h = int(seg / me.nrb);
+    const int64_t begin = u0 - (at - seg * (me.tiles + 1));
+    if (lane == 0)
+      write_cut(ar.cuts + id, me.tile > 0, begin, begin + 1, me.tiles, U, W, me.rb, me.n, me.q0, me.h);
   }
   auto advance = [&](Cursor& s) {
     ++s.at;
@@ -635,97 +633,29 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   cp_wait<0>();
 }
 
-// Joins the parts of cut segments: one CTA per (sequence, head, row block),
-// RB x 32 threads times GROUPS; group k takes parts k, k + GROUPS, ... of its
-// row in order, and the groups are added in order.
+// Joins the parts of cut segments: a block of 8 warps for each start of a run, one
+// row of the segment per warp, or more warps to a row where it has many parts.
 template <typename TQ, int D>
-__global__ void __launch_bounds__(1024)
-    attn_kv8_join_kernel(TQ* __restrict__ O, Cache c, Batch bt, Args ar, int64_t total_warps,
-                         int most_rb) {
-  constexpr int GROUPS = 32 / RB, PER = D / 32;  // elements per lane
-  __shared__ float sm[GROUPS][RB], sl[GROUPS][RB];
-  __shared__ float so[GROUPS][RB][D];
+__global__ void __launch_bounds__(256, 5)
+    attn_kv8_join_kernel(TQ* __restrict__ O, Args ar) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int64_t id = blockIdx.x;
-  const int rb = int(id % most_rb);
-  id /= most_rb;
-  const int h = int(id % c.heads), b = int(id / c.heads);
-  Cursor s;
-  s.b = b;
-  s.load(bt, c.tshift, ar.G, Shape<D>::TK, nullptr);
-  if (s.n == 0 || rb >= s.nrb) return;
-  const int64_t U = ar.prefix[bt.B], W = workers(U, total_warps);
-  const int64_t f = ar.prefix[b] + (int64_t(h) * s.nrb + rb) * (s.tiles + 1) + 1;
-  const int64_t wa = run_owner(f, U, W), wb = run_owner(f + s.tiles - 1, U, W);
-  if (wa == wb) return;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = warp % RB, grp = warp / RB;
-  float m = -CUDART_INF_F, l = 0.f, o[PER] = {};
-  // a worker's first segment is its part 0, a later (cut) one its part 1
-  for (int64_t w0 = wa + grp; w0 <= wb; w0 += GROUPS * 8) {
-    float pm[8], pl[8], po[8][PER];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t w = w0 + k * GROUPS;
-      pm[k] = -CUDART_INF_F, pl[k] = 0.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) po[k][e] = 0.f;
-      if (w <= wb) {
-        const int64_t row = (w * 2 + (run_start(w, U, W) >= f - 1 ? 0 : 1)) * RB + r;
-        pm[k] = __ldcg(ar.part_ml + row * 2);
-        pl[k] = __ldcg(ar.part_ml + row * 2 + 1);
-#pragma unroll
-        for (int e = 0; e < PER; ++e) po[k][e] = __ldcg(ar.parts + row * D + e * 32 + lane);
-      }
-    }
-    float now = m;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) now = fmaxf(now, pm[k]);
-    if (now == -CUDART_INF_F) now = 0.f;
-    const float a = exp2_approx(m - now);
-    m = now;
-    l *= a;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] *= a;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = exp2_approx(pm[k] - now);
-      l = fmaf(pl[k], x, l);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = fmaf(po[k][e], x, o[e]);
-    }
-  }
-  if (lane == 0) sm[grp][r] = m, sl[grp][r] = l;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) so[grp][r][e * 32 + lane] = o[e];
-  __syncthreads();
-  if (grp != 0) return;
-  float now = -CUDART_INF_F;
-#pragma unroll
-  for (int k = 0; k < GROUPS; ++k) now = fmaxf(now, sm[k][r]);
-  if (now == -CUDART_INF_F) now = 0.f;
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = 0.f;
-#pragma unroll
-  for (int k = 0; k < GROUPS; ++k) {
-    const float x = exp2_approx(sm[k][r] - now);
-    l = fmaf(sl[k][r], x, l);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = fmaf(so[k][r][e * 32 + lane], x, o[e]);
-  }
-  const int rr = rb * RB + r;
-  if (rr >= s.n * ar.G) return;
+  const int w = 1 + int(blockIdx.x);
+  const Cut cut = ar.cuts[w];
+  JoinShare js;
+  if (!join_share(w, cut, &js)) return;
+  float l, o[D / 32];
+  if (!join_row<D>(js, cut, RB, js.row, ar.parts, ar.part_ml, &l, o)) return;
+  const int rr = cut.rows * RB + js.row;
+  if (rr >= cut.n * ar.G) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = rr / ar.G;
-  TQ* dst = O + (int64_t(s.q0 + i) * ar.heads + h * ar.G + (rr - i * ar.G)) * D;
+  TQ* dst = O + (int64_t(cut.q0 + i) * ar.heads + cut.h * ar.G + (rr - i * ar.G)) * D;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
+  for (int e = 0; e < D / 32; ++e) {
     if constexpr (std::is_same<TQ, __half>::value)
-      dst[e * 32 + lane] = __float2half_rn(o[e] * inv);
+      dst[e * 32 + (threadIdx.x & 31)] = __float2half_rn(o[e] * inv);
     else
-      dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+      dst[e * 32 + (threadIdx.x & 31)] = __float2bfloat16_rn(o[e] * inv);
   }
 }
 
@@ -739,14 +669,14 @@ namespace {
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Ws {
-  size_t ml, prefix, bytes;
+  size_t ml, cuts, bytes;
 };
-Ws attn_ws(int64_t B, int64_t D) {
+Ws attn_ws(int64_t D) {
   const size_t w2 = size_t(sm_count()) * wq::kv8::MAX_WARPS * 2, rb = size_t(wq::kv8::RB);
   Ws s;
   s.ml = up256(w2 * rb * size_t(D) * 4);
-  s.prefix = s.ml + up256(w2 * rb * 8);
-  s.bytes = s.prefix + up256(size_t(B + 1) * 8);
+  s.cuts = s.ml + up256(w2 * rb * 8);
+  s.bytes = s.cuts + w2 / 2 * sizeof(wq::kv8::Cut);
   return s;
 }
 
@@ -775,27 +705,23 @@ int launch_decode(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int m
                 int(a.kv_heads), tshift};
   const Batch bt{a.table, a.cu, a.lens, int(a.B), int(a.width), int(a.rows), int(a.max_new)};
   const Rope rp{a.cos, a.sin, int(a.rot), max_pos, a.interleaved};
-  const Ws w = attn_ws(a.B, D);
+  const Ws w = attn_ws(D);
   const Args ar{ldq, int(heads), G, scale * 1.4426950408889634f, reinterpret_cast<float*>(ws),
-                reinterpret_cast<float*>(ws + w.ml), reinterpret_cast<int64_t*>(ws + w.prefix)};
+                reinterpret_cast<float*>(ws + w.ml), reinterpret_cast<Cut*>(ws + w.cuts)};
   const int grid = sm_count();
   TQ* o = static_cast<TQ*>(out);
   kern<<<grid, WARPS * 32, smem, s>>>(static_cast<const TQ*>(Q), o, c, bt, rp, ar, status_ptr());
   WQ_LAUNCH_CHECK("attn_kv8_kernel");
-  const int64_t most_rb = (a.max_new * G + RB - 1) / RB;
-  const int64_t joins = a.B * a.kv_heads * most_rb;
-  if (joins > 0x7fffffff) return WQ_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(joins));
-  cfg.blockDim = dim3(1024);
+  cfg.gridDim = dim3(unsigned(grid * WARPS - 1));
+  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<TQ, D>, o, c, bt, ar,
-                                   int64_t(grid) * WARPS, int(most_rb)));
+  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_join_kernel<TQ, D>, o, ar));
   return WQ_OK;
 }
 
@@ -809,11 +735,10 @@ int launch_by_shape(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int
 
 }  // namespace
 
-size_t attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
-                                int64_t max_q) {
+size_t attn_kv8_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
   if (attn_kv8_on_tc(heads, kv_heads, D, max_q))
-    return attn_kv8_tc_workspace_bytes(B, heads, kv_heads, D, max_q);
-  return attn_ws(B, D).bytes;
+    return attn_kv8_tc_workspace_bytes(heads, kv_heads, D, max_q);
+  return attn_ws(D).bytes;
 }
 
 int launch_attn_kv8(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,

@@ -100,7 +100,7 @@ struct TcArgs {
   float scale_log2;
   float* parts;     // [2 W][ROWS][D]
   float* part_ml;   // [2 W][ROWS][2]
-  int64_t* prefix;  // [B most_r + 1] first unit of each (sequence, row tile)
+  Cut* cuts;        // [W] the items that the runs' starts cut
 };
 
 // An item's (sequence, row tile) and how many blocks it has.
@@ -212,10 +212,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           sm.start_p = p;
           sm.start_off = u0 - first;
         }
-        if (blockIdx.x == 0 && p < P) {
-          ar.prefix[p] = first;
-          if (p == P - 1) ar.prefix[P] = U;
-        }
       }
       __syncthreads();
     }
@@ -224,10 +220,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t W = workers(U, gridDim.x);
       u0 = U && blockIdx.x < W ? run_start(blockIdx.x, U, W) : -1;
       u1 = U && blockIdx.x < W ? run_start(blockIdx.x + 1, U, W) : -1;
-      if (U == 0) return;
+      if (U == 0) break;
     }
   }
-  if (u0 < 0) return;
+  if (U == 0 || u0 < 0) {
+    if (threadIdx.x == 0) write_cut(ar.cuts + blockIdx.x, false, 0, 0, 0, 0, 0, 0, 0, 0, 0);
+    return;
+  }
   Walk wk;
   wk.u0 = u0, wk.u1 = u1;
   wk.it.b = sm.start_p / ar.most_r;
@@ -236,6 +235,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   wk.it.h = int(sm.start_off / (wk.it.tiles + START));
   wk.begin = u0 - (sm.start_off - int64_t(wk.it.h) * (wk.it.tiles + START));
   wk.clip();
+  if (threadIdx.x == 0)
+    write_cut(ar.cuts + blockIdx.x, wk.t0 > 0, wk.begin, wk.begin + START, wk.it.tiles, U,
+              workers(U, gridDim.x), wk.it.r, wk.it.n, wk.it.q0, wk.it.h);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -656,80 +658,27 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the parts of cut items: a warp per row, parts in order.
+// Joins the parts of cut items: blocks as in attn_kv8.cu, for each 8 rows.
 template <typename TQ, int D, bool PAIR>
-__global__ void __launch_bounds__(256)
-    attn_kv8_tc_join_kernel(TQ* __restrict__ O, Cache c, Batch bt, TcArgs ar, int64_t workers_max) {
-  constexpr int ROWS = PAIR ? 256 : 128, PER = D / 32;
+__global__ void __launch_bounds__(256, 5) attn_kv8_tc_join_kernel(TQ* __restrict__ O, TcArgs ar) {
+  constexpr int ROWS = PAIR ? 256 : 128;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  // the item that the boundary in front of run w cuts, if no earlier one does
-  const int64_t w = 1 + blockIdx.x / (ROWS / 8);
-  const int P = bt.B * ar.most_r, oct = int(blockIdx.x % (ROWS / 8));
-  const int64_t U = ar.prefix[P], W = workers(U, workers_max);
-  if (w >= W) return;
-  const int64_t u = run_start(w, U, W);
-  int p = 0;
-  for (int hi = P; hi - p > 1;) {  // the last p with prefix[p] <= u
-    const int mid = (p + hi) / 2;
-    if (ar.prefix[mid] <= u)
-      p = mid;
-    else
-      hi = mid;
-  }
-  Item it;
-  it.b = p / ar.most_r;
-  it.r = p - it.b * ar.most_r;
-  it.load(bt, c.tshift, ar.G, ROWS, nullptr);
-  const int h = int((u - ar.prefix[p]) / (it.tiles + START));
-  const int row = oct * 8 + (threadIdx.x >> 5), rr = it.r * ROWS + row;
-  if (rr >= it.n * ar.G) return;
-  const int64_t begin = ar.prefix[p] + int64_t(h) * (it.tiles + START), f = begin + START;
-  const int64_t wa = run_owner(f, U, W), wb = run_owner(f + it.tiles - 1, U, W);
-  if (wa != w - 1 || wa == wb) return;
-  float m = -CUDART_INF_F, l = 0.f, o[PER] = {};
-  for (int64_t w0 = wa; w0 <= wb; w0 += 4) {
-    float pm[4], pl[4], po[4][PER];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t w = w0 + k;
-      pm[k] = -CUDART_INF_F, pl[k] = 0.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) po[k][e] = 0.f;
-      if (w <= wb) {
-        const int64_t at = (w * 2 + (run_start(w, U, W) >= begin ? 0 : 1)) * ROWS + row;
-        pm[k] = __ldcg(ar.part_ml + at * 2);
-        pl[k] = __ldcg(ar.part_ml + at * 2 + 1);
-#pragma unroll
-        for (int e = 0; e < PER; ++e) po[k][e] = __ldcg(ar.parts + at * D + e * 32 + lane);
-      }
-    }
-    float now = m;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) now = fmaxf(now, pm[k]);
-    if (now == -CUDART_INF_F) now = 0.f;
-    const float a = exp2_approx(m - now);
-    m = now;
-    l *= a;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] *= a;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = exp2_approx(pm[k] - now);
-      l = fmaf(pl[k], x, l);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = fmaf(po[k][e], x, o[e]);
-    }
-  }
+  const int w = 1 + int(blockIdx.x) / (ROWS / 8), oct = int(blockIdx.x) % (ROWS / 8);
+  const Cut cut = ar.cuts[w];
+  JoinShare js;
+  if (cut.rows * int64_t(ROWS) + oct * 8 >= int64_t(cut.n) * ar.G || !join_share(w, cut, &js)) return;
+  const int row = oct * 8 + js.row, rr = cut.rows * ROWS + row;
+  float l, o[D / 32];
+  if (!join_row<D>(js, cut, ROWS, row, ar.parts, ar.part_ml, &l, o) || rr >= cut.n * ar.G) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = rr / ar.G;
-  TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + h * ar.G + (rr - i * ar.G)) * D;
+  TQ* dst = O + (int64_t(cut.q0 + i) * ar.heads + cut.h * ar.G + (rr - i * ar.G)) * D;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
+  for (int e = 0; e < D / 32; ++e) {
     if constexpr (std::is_same<TQ, __half>::value)
-      dst[e * 32 + lane] = __float2half_rn(o[e] * inv);
+      dst[e * 32 + (threadIdx.x & 31)] = __float2half_rn(o[e] * inv);
     else
-      dst[e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+      dst[e * 32 + (threadIdx.x & 31)] = __float2bfloat16_rn(o[e] * inv);
   }
 }
 
@@ -744,14 +693,14 @@ namespace {
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct TcWs {
-  size_t ml, prefix, bytes;
+  size_t ml, cuts, bytes;
 };
-TcWs tc_ws(int64_t B, int64_t max_rows, int64_t D, bool pair) {
+TcWs tc_ws(int64_t D, bool pair) {
   const size_t rows = pair ? 256 : 128, w2 = size_t(sm_count()) * 2;
   TcWs s;
   s.ml = up256(w2 * rows * size_t(D) * 4);
-  s.prefix = s.ml + up256(w2 * rows * 8);
-  s.bytes = s.prefix + up256(size_t(B * ((max_rows + int64_t(rows) - 1) / int64_t(rows)) + 1) * 8);
+  s.cuts = s.ml + up256(w2 * rows * 8);
+  s.bytes = s.cuts + w2 / 2 * sizeof(wq::kv8::Cut);
   return s;
 }
 
@@ -783,10 +732,10 @@ int launch_tc(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int max_p
                 int(a.kv_heads), tshift};
   const Batch bt{a.table, a.cu, a.lens, int(a.B), int(a.width), int(a.rows), int(a.max_new)};
   const Rope rp{a.cos, a.sin, int(a.rot), max_pos, a.interleaved};
-  const TcWs w = tc_ws(a.B, a.max_new * G, D, PAIR);
+  const TcWs w = tc_ws(D, PAIR);
   const TcArgs ar{ldq, int(heads), G, int(most_r), scale * 1.4426950408889634f,
                   reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + w.ml),
-                  reinterpret_cast<int64_t*>(ws + w.prefix)};
+                  reinterpret_cast<Cut*>(ws + w.cuts)};
   const int grid = sm_count();
   TQ* o = static_cast<TQ*>(out);
   kern<<<grid, THREADS, smem, s>>>(static_cast<const TQ*>(Q), o, c, bt, rp, ar, status_ptr(),
@@ -802,8 +751,7 @@ int launch_tc(const void* Q, int64_t ldq, int64_t heads, const Kv8& a, int max_p
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_tc_join_kernel<TQ, D, PAIR>, o, c, bt, ar,
-                                   int64_t(grid)));
+  WQ_CUDA_CHECK(cudaLaunchKernelEx(&cfg, attn_kv8_tc_join_kernel<TQ, D, PAIR>, o, ar));
   return WQ_OK;
 }
 
@@ -828,12 +776,10 @@ bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
   return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
 }
 
-size_t attn_kv8_tc_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+size_t attn_kv8_tc_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t D,
                                    int64_t max_q) {
   const int64_t rows = max_q * (heads / kv_heads);
-  const size_t one = tc_ws(B, rows, D, false).bytes;
-  const size_t two = rows > 128 ? tc_ws(B, rows, D, true).bytes : 0;
-  return one > two ? one : two;
+  return tc_ws(D, rows > 128).bytes;  // (pairs of row tiles need the more)
 }
 
 int launch_attn_kv8_tc(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,

@@ -100,12 +100,10 @@ struct Kv8 {
 };
 int launch_kv8_append(const void* K, const void* V, int dtype, int64_t ldk, int64_t ldv,
                       const Kv8& a, int max_pos, cudaStream_t s);
-size_t attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
-                                int64_t max_q);
+size_t attn_kv8_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q);
 bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q);
 bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q);
-size_t attn_kv8_tc_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
-                                   int64_t max_q);
+size_t attn_kv8_tc_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q);
 int launch_attn_kv8_tc(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,
                        int max_pos, float scale, void* out, void* ws, cudaStream_t s);
 int launch_attn_kv8(const void* Q, int dtype, int64_t ldq, int64_t heads, const Kv8& a,

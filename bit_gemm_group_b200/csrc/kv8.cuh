@@ -130,5 +130,119 @@ __device__ __forceinline__ int64_t workers(int64_t U, int64_t W) {
   return w < W ? w : W;
 }
 
+// ------------------------------------------------------------------- joining
+// What run w (w > 0) says about its start: whether that cuts a segment (first_run
+// >= 0), which, and the runs first_run .. last_run that have parts of it.  A run's
+// first segment is its part 0; only the first run can have begun with an earlier
+// one, and then holds this one as its part 1.
+struct __align__(16) Cut {
+  int first_run, last_run, first_part, rows;  // rows: row block (row tile) of the segment
+  int n, q0, h, pad;                          // of its sequence; kv head
+};
+
+// Written by one thread for each run, cutting or not.
+__device__ __forceinline__ void write_cut(Cut* cut, bool cuts, int64_t begin, int64_t first_unit,
+                                          int tiles, int64_t U, int64_t W, int rows, int n, int q0,
+                                          int h) {
+  int4 a = make_int4(-1, 0, 0, 0), b = make_int4(0, 0, 0, 0);
+  if (cuts) {
+    const int64_t wa = run_owner(first_unit, U, W);
+    a = make_int4(int(wa), int(run_owner(first_unit + tiles - 1, U, W)),
+                  run_start(wa, U, W) < begin ? 1 : 0, rows);
+    b = make_int4(n, q0, h, 0);
+  }
+  reinterpret_cast<int4*>(cut)[0] = a;
+  reinterpret_cast<int4*>(cut)[1] = b;
+}
+
+// A block of 8 warps at the start of run w.  The blocks of a segment's cuts share
+// the work on 8 of its rows: `split` of them (a power of two up to 8) take part,
+// block i the 8 / split rows from i * 8 / split on, with `split` warps per row.
+struct JoinShare {
+  int row, group, groups;  // this warp's row of the 8, its share of the parts
+};
+__device__ __forceinline__ bool join_share(int w, const Cut& c, JoinShare* js) {
+  if (c.first_run < 0) return false;
+  const int cuts = c.last_run - c.first_run, i = w - 1 - c.first_run;
+  const int split = cuts >= 8 ? 8 : cuts >= 4 ? 4 : cuts >= 2 ? 2 : 1;
+  if (i >= split) return false;
+  const int warp = threadIdx.x >> 5, rows = 8 / split;
+  js->row = i * rows + warp / split;
+  js->group = warp % split;
+  js->groups = split;
+  return true;
+}
+
+// The sum of a row's parts of the runs first + group, first + group + groups, ...
+// in order (l and, in lane e' of each 32, elements e 32 + e' of o), then of the
+// groups in order through shared memory; true in the warp that holds the row.
+// `row` of `rows` is the row's place in a part.
+template <int D>
+__device__ __forceinline__ bool join_row(const JoinShare& js, const Cut& cut, int rows, int row,
+                                         const float* parts, const float* part_ml, float* l_out,
+                                         float (&o)[D / 32]) {
+  constexpr int PER = D / 32, BATCH = D == 256 ? 2 : 4;
+  __shared__ float sm[8][2], so[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -__int_as_float(0x7f800000), l = 0.f;
+  const float none = m;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) o[e] = 0.f;
+  for (int w0 = cut.first_run + js.group; w0 <= cut.last_run; w0 += js.groups * BATCH) {
+    float pm[BATCH], pl[BATCH], po[BATCH][PER];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {  // (all in flight before the first is used)
+      const int w = w0 + k * js.groups;
+      pm[k] = none, pl[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) po[k][e] = 0.f;
+      if (w <= cut.last_run) {
+        const int64_t r = int64_t(w * 2 + (w == cut.first_run ? cut.first_part : 0)) * rows + row;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + r * 2));
+        pm[k] = ml.x, pl[k] = ml.y;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) po[k][e] = __ldcg(parts + r * D + e * 32 + lane);
+      }
+    }
+    float now = m;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) now = fmaxf(now, pm[k]);
+    if (now == none) now = 0.f;
+    const float a = exp2_approx(m - now);
+    m = now;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] *= a;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float x = exp2_approx(pm[k] - now);
+      l = fmaf(pl[k], x, l);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(po[k][e], x, o[e]);
+    }
+  }
+  if (js.groups > 1) {
+    if (lane == 0) sm[warp][0] = m, sm[warp][1] = l;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) so[warp][e * 32 + lane] = o[e];
+    __syncthreads();
+    if (js.group != 0) return false;
+    float now = none;
+    for (int k = 0; k < js.groups; ++k) now = fmaxf(now, sm[warp + k][0]);
+    if (now == none) now = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int k = 0; k < js.groups; ++k) {
+      const float x = exp2_approx(sm[warp + k][0] - now);
+      l = fmaf(sm[warp + k][1], x, l);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(so[warp + k][e * 32 + lane], x, o[e]);
+    }
+  }
+  *l_out = l;
+  return true;
+}
+
 }  // namespace kv8
 }  // namespace wq

@@ -485,7 +485,7 @@ size_t wq_attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, i
   if (B <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || D <= 0 || max_new <= 0)
     return 0;
   wq_host::ensure_device();  // the size depends on the device's SM count
-  return wq_host::attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new);
+  return wq_host::attn_kv8_workspace_bytes(heads, kv_heads, D, max_new);
 }
 
 int wq_attn_kv8(const void* Q, int dtype, int64_t n, int64_t ldq, int64_t heads, int64_t kv_heads,
@@ -514,7 +514,7 @@ int wq_attn_kv8(const void* Q, int dtype, int64_t n, int64_t ldq, int64_t heads,
   if (!ws) return WQ_ERR_WORKSPACE;
   st = wq_host::ensure_device();
   if (st != WQ_OK) return st;
-  if (ws_bytes < wq_host::attn_kv8_workspace_bytes(B, heads, kv_heads, D, max_new))
+  if (ws_bytes < wq_host::attn_kv8_workspace_bytes(heads, kv_heads, D, max_new))
     return WQ_ERR_WORKSPACE;
   const wq_host::Kv8 a{const_cast<void*>(kq), const_cast<void*>(vq),
                        static_cast<float*>(const_cast<void*>(ks)),
