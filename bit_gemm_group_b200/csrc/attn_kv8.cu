@@ -296,11 +296,42 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     pg1 = T_ < TK && ((col + 1) << c.tshift) < s.len ? __ldg(row + 1) : -1;
   };
   pages_of(ahead);
-  auto issue = [&]() {
-    if (ahead.at < count) {
-      const uint32_t st = base + uint32_t(issued % S::STAGES) * S::STAGE;
+  // a unit's keys (and scales) are requested as soon as the buffer's last ones
+  // have been used, its values when those have: STAGES units on their way
+  constexpr int PER = D / 16, STEP = 32 / PER, COPIES = TK / STEP;
+  const int copy_row = lane / PER, piece = lane % PER;
+  int64_t from0 = 0, from1 = 0;  // of the unit whose keys were requested last
+  int rows = 0;
+  bool ok0 = false, ok1 = false, live = false;
+  // rows are contiguous in a page, so a lane's pieces are 512 bytes apart
+  auto request = [&](const uint8_t* src, uint32_t dst, int pitch) {
+    if (live) {
+      if (T_ >= TK && ok0 && rows >= TK) {
+        const uint8_t* p = src + from0;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int r = copy_row + i * STEP;
+          cp16(dst + r * pitch + swz(D, r, piece) * 16, p + i * 512);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          const int r = copy_row + i * STEP;
+          const bool second = T_ < TK && i >= COPIES / 2;
+          cp16z(dst + r * pitch + swz(D, r, piece) * 16, src + (second ? from1 : from0) + i * 512,
+                r < rows && (second ? ok1 : ok0));
+        }
+      }
+    }
+    cp_commit();
+  };
+  auto request_keys = [&]() {
+    live = ahead.at < count;
+    const uint32_t st = base + uint32_t(issued % S::STAGES) * S::STAGE;
+    if (live) {
       const int tok0 = ahead.tile * TK, col = tok0 >> c.tshift;
-      const bool ok0 = pg0 >= 0 && pg0 < c.pages, ok1 = pg1 >= 0 && pg1 < c.pages;
+      ok0 = pg0 >= 0 && pg0 < c.pages, ok1 = pg1 >= 0 && pg1 < c.pages;
+      rows = ahead.len - tok0;
       if (lane < 2 && (lane == 0 || T_ < TK)) {
         const bool ok = lane ? ok1 : ok0, used = ((col + lane) << c.tshift) < ahead.len;
         const uint32_t sc = st + S::KBYTES + S::VBYTES + 8 * lane;
@@ -315,39 +346,22 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
           if (used) record_error(status, WQ_ERR_ARG);
         }
       }
-      // rows are contiguous in a page, so a lane's pieces are 512 bytes apart
-      constexpr int PER = D / 16, STEP = 32 / PER, COPIES = TK / STEP;
-      const int rows = ahead.len - tok0, r0 = lane / PER, piece = lane % PER;
-      const int64_t at0 = ((c.block(ok0 ? pg0 : 0, ahead.h) << c.tshift) + (tok0 & (T_ - 1))) * D + lane * 16;
-      if (T_ >= TK && ok0 && rows >= TK) {
-        const uint8_t *pk = c.kq + at0, *pv = c.vq + at0;
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const int r = r0 + i * STEP;
-          cp16(st + r * S::KP + swz(D, r, piece) * 16, pk + i * 512);
-          cp16(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, pv + i * 512);
-        }
-      } else {
-        const int64_t at1 =
-            T_ < TK ? (c.block(ok1 ? pg1 : 0, ahead.h) << c.tshift) * D + lane * 16 - 16 * D : at0;
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          const int r = r0 + i * STEP;
-          const bool second = T_ < TK && i >= COPIES / 2;
-          const bool valid = r < rows && (second ? ok1 : ok0);
-          const int64_t at = (second ? at1 : at0) + i * 512;
-          cp16z(st + r * S::KP + swz(D, r, piece) * 16, c.kq + at, valid);
-          cp16z(st + S::KBYTES + r * S::VP + swz(D, r, piece) * 16, c.vq + at, valid);
-        }
-      }
-      ++issued;
+      from0 = ((c.block(ok0 ? pg0 : 0, ahead.h) << c.tshift) + (tok0 & (T_ - 1))) * D + lane * 16;
+      from1 = T_ < TK ? (c.block(ok1 ? pg1 : 0, ahead.h) << c.tshift) * D + lane * 16 - 16 * D : from0;
       advance(ahead);
       if (ahead.at < count) pages_of(ahead);
     }
-    cp_commit();
+    request(c.kq, st, S::KP);
+  };
+  auto request_values = [&]() {
+    request(c.vq, base + uint32_t(issued % S::STAGES) * S::STAGE + S::KBYTES, S::VP);
+    ++issued;
   };
 #pragma unroll
-  for (int i = 0; i < S::STAGES - 1; ++i) issue();
+  for (int i = 0; i < S::STAGES; ++i) {
+    request_keys();
+    request_values();
+  }
 
   uint32_t qa[KS][4];
   float acc[MT][4];
@@ -453,11 +467,23 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
     }
-    cp_wait<S::STAGES - 2>();
+    cp_wait<2 * S::STAGES - 1>();
     __syncwarp();
-    issue();
     const uint32_t st = base + uint32_t(u % S::STAGES) * S::STAGE;
     const uint32_t vb = st + S::KBYTES, scb = vb + S::VBYTES;
+
+    // (the unit's second page, where it has two, is that of the upper half)
+    auto page_scales = [&](int k, float& f, float& lv, float& rv) {
+      const float ks = lds32f(scb + 8 * k), vs = lds32f(scb + 8 * k + 4);
+      const float v = fmaxf(vs, 1e-30f);
+      f = fq * ks;
+      lv = vs < 0.f ? -CUDART_INF_F : __log2f(v);
+      rv = __fdividef(1.f, v);
+    };
+    float f0, lv0, rv0, f1, lv1, rv1;
+    page_scales(0, f0, lv0, rv0);
+    f1 = f0, lv1 = lv0, rv1 = rv0;
+    if (T_ < TK) page_scales(1, f1, lv1, rv1);
 
     // -------------------------------------------------- scores
     float sc[NT][4];
@@ -484,19 +510,10 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
       }
     }
 
+    __syncwarp();
+    request_keys();
+
     // -------------------------------------------------- softmax, base 2
-    // (the unit's second page, where it has two, is that of the upper half)
-    auto page_scales = [&](int k, float& f, float& lv, float& rv) {
-      const float ks = lds32f(scb + 8 * k), vs = lds32f(scb + 8 * k + 4);
-      const float v = fmaxf(vs, 1e-30f);
-      f = fq * ks;
-      lv = vs < 0.f ? -CUDART_INF_F : __log2f(v);
-      rv = __fdividef(1.f, v);
-    };
-    float f0, lv0, rv0, f1, lv1, rv1;
-    page_scales(0, f0, lv0, rv0);
-    f1 = f0, lv1 = lv0, rv1 = rv0;
-    if (T_ < TK) page_scales(1, f1, lv1, rv1);
     float mx = -CUDART_INF_F;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -549,6 +566,8 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     }
 
     // -------------------------------------------------- values
+    cp_wait<2 * S::STAGES - 1>();
+    __syncwarp();
 #pragma unroll
     for (int ks = 0; ks < TK / 16; ++ks) {
       const int r = ks * 16 + 2 * t;
@@ -576,6 +595,9 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
         }
       }
     }
+
+    __syncwarp();
+    request_values();
 
     // -------------------------------------------------- end of a segment
     const bool last = me.tile + 1 == me.tiles || me.at + 1 >= count;
