@@ -16,9 +16,10 @@
 // Work is cut into units of TK positions of one (sequence, head, row block),
 // numbered with the position fastest, and every warp of the grid takes an
 // equal run of them, whatever the sequences' lengths: no warp waits for
-// another.  A segment (all units of a row block) counts one unit more, for its
-// queries and its result: without it the warps that got many short sequences
-// ended a quarter later than the rest.  A run's whole segments are written out directly; cut ones go to
+// another.  A segment (all units of a row block) counts two units more, for its
+// queries and its result: a unit takes a warp 2.6 us in a full decode step, a
+// segment's start and end about 5, and without that the warps that got many
+// short sequences ended a quarter later than the rest.  A run's whole segments are written out directly; cut ones go to
 // the workspace and attn_kv8_join_kernel adds them in a fixed order.
 //
 // Softmax in one pass, in base 2, with the value scale folded into the
@@ -39,6 +40,7 @@ namespace kv8 {
 
 constexpr int MAX_WARPS = 12;
 constexpr int RB = 8;      // rows per block
+constexpr int START = 2;   // units that a segment's queries and result count
 
 template <int D_>
 struct Shape {
@@ -167,7 +169,7 @@ struct Cursor {
     tiles = len > 0 ? (len + TK - 1) / TK : 1;
   }
   __device__ __forceinline__ int64_t units(int heads) const {
-    return n > 0 ? int64_t(nrb) * heads * (tiles + 1) : 0;
+    return n > 0 ? int64_t(nrb) * heads * (tiles + START) : 0;
   }
 };
 
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   constexpr int KS = D / 16;  // steps of the product over D
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t warp_sum[WARPS], start_at[WARPS], run_at[WARPS];
-  __shared__ int start_b[WARPS];
+  __shared__ Cursor start_seq[WARPS];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,76 +199,67 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   const int T_ = 1 << c.tshift;
 
   // ------------------------------------------------ which units are this warp's
-  Cursor me;
-  int64_t U = 0, u0 = 0, u1 = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t run = 0;
-    for (int b0 = 0; b0 < bt.B; b0 += WARPS * 32) {
-      Cursor s;
-      s.b = b0 + int(threadIdx.x);
-      int64_t mine = 0;
-      if (s.b < bt.B) {
-        s.load(bt, c.tshift, ar.G, TK, pass ? nullptr : status);
-        mine = s.units(c.heads);
-      }
-      int64_t inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) warp_sum[warp] = inc;
-      __syncthreads();
-      int64_t before = run;
-      for (int w = 0; w < warp; ++w) before += warp_sum[w];
-      for (int w = 0; w < WARPS; ++w) run += warp_sum[w];
-      const int64_t first = before + inc - mine;
-      if (pass == 1) {
-        // the sequence that holds a warp's first unit
-        for (int w = 0; w < WARPS; ++w) {
-          const int64_t u = run_at[w];
-          if (mine > 0 && u >= first && u < first + mine) {
-            start_b[w] = s.b;
-            start_at[w] = u - first;
-          }
+  constexpr int NT_ = WARPS * 32;
+  auto units_at = [&](Cursor& s, int b, int* st) {
+    s.b = b;
+    if (b >= bt.B) return int64_t(0);
+    s.load(bt, c.tshift, ar.G, TK, st);
+    return s.units(c.heads);
+  };
+  // (up to 384 sequences are looked at once)
+  const bool one = bt.B <= NT_;
+  Cursor mine;
+  int64_t U = 0, part = 0, first = 0, units = 0;
+  for (int b0 = 0; b0 < bt.B; b0 += NT_) {
+    units = units_at(mine, b0 + int(threadIdx.x), status);
+    first = U + block_scan<WARPS>(units, warp_sum, &part);
+    U += part;
+  }
+  const Runs runs(U, int64_t(gridDim.x) * WARPS);
+  if (threadIdx.x < WARPS) {
+    const int id = int(threadIdx.x) * gridDim.x + blockIdx.x;
+    run_at[threadIdx.x] = id < runs.workers ? runs.start(id) : -1;
+  }
+  __syncthreads();
+  int64_t done = 0;
+  for (int b0 = 0; b0 < bt.B; b0 += NT_) {
+    if (!one) {
+      units = units_at(mine, b0 + int(threadIdx.x), nullptr);
+      first = done + block_scan<WARPS>(units, warp_sum, &part);
+      done += part;
+    }
+    // the sequence that holds a warp's first unit
+    if (units > 0)
+      for (int w = 0; w < WARPS; ++w) {
+        const int64_t u = run_at[w];
+        if (u >= first && u < first + units) {
+          start_seq[w] = mine;
+          start_at[w] = u - first;
         }
       }
-      __syncthreads();
-    }
-    U = run;
-    if (pass == 0 && threadIdx.x < WARPS) {
-      const int64_t W = workers(U, int64_t(gridDim.x) * WARPS);
-      const int64_t id = int64_t(threadIdx.x) * gridDim.x + blockIdx.x;
-      run_at[threadIdx.x] = id < W ? run_start(id, U, W) : -1;
-    }
-    __syncthreads();
-    if (U == 0) break;
   }
-  const int64_t W = workers(U, int64_t(gridDim.x) * WARPS);
-  const int64_t id = int64_t(warp) * gridDim.x + blockIdx.x;
-  if (id >= W) {
-    if (lane == 0) write_cut(ar.cuts + id, false, 0, 0, 0, 0, 0, 0, 0, 0, 0);
+  __syncthreads();
+  const int id = warp * gridDim.x + blockIdx.x;
+  if (id >= runs.workers) {
+    if (lane == 0) write_cut(ar.cuts + id, false, runs, 0, 0, 0, 0, 0, 0, 0);
     return;
   }
-  u0 = run_start(id, U, W);
-  u1 = run_start(id + 1, U, W);
-  me.b = start_b[warp];
-  me.load(bt, c.tshift, ar.G, TK, nullptr);
-  {
-    const int64_t at = start_at[warp], seg = at / (me.tiles + 1);
-    me.at = 0;
-    me.tile = int(at - seg * (me.tiles + 1)) - 1;
-    if (me.tile < 0) me.tile = 0, me.at = 1;  // the run begins with the segment's own unit
-    me.rb = int(seg % me.nrb);
-    me.h = int(seg / me.nrb);
-    const int64_t begin = u0 - (at - seg * (me.tiles + 1));
-    if (lane == 0)
-      write_cut(ar.cuts + id, me.tile > 0, begin, begin + 1, me.tiles, U, W, me.rb, me.n, me.q0, me.h);
-  }
+  const int64_t u0 = run_at[warp];
+  const int count = int(runs.start(id + 1) - u0);
+  Cursor me = start_seq[warp];
+  const int64_t at_seq = start_at[warp], seg = quotient(at_seq, me.tiles + START);
+  const int64_t seg_begin = u0 - (at_seq - seg * (me.tiles + START));
+  me.tile = int(u0 - seg_begin) - START;
+  me.at = me.tile < 0 ? -me.tile : 0;  // units of the segment's start
+  if (me.tile < 0) me.tile = 0;
+  me.h = int(quotient(seg, me.nrb));
+  me.rb = int(seg - int64_t(me.h) * me.nrb);
+  const bool cuts = me.tile > 0;
+  const int cut_tiles = me.tiles, cut_rb = me.rb, cut_n = me.n, cut_q0 = me.q0, cut_h = me.h;
   auto advance = [&](Cursor& s) {
     ++s.at;
     if (++s.tile < s.tiles) return;
-    ++s.at;
+    s.at += START;
     s.tile = 0;
     if (++s.rb < s.nrb) return;
     s.rb = 0;
@@ -287,7 +280,6 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   // ------------------------------------------------ the copies, a few units ahead
   Cursor ahead = me;
   int issued = 0;
-  const int count = int(u1 - u0);
   int pg0 = -1, pg1 = -1;  // the pages of the unit to be copied next
   auto pages_of = [&](const Cursor& s) {
     const int col = (s.tile * TK) >> c.tshift;
@@ -362,6 +354,8 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     request_keys();
     request_values();
   }
+  if (lane == 0)
+    write_cut(ar.cuts + id, cuts, runs, seg_begin, START, cut_tiles, cut_rb, cut_n, cut_q0, cut_h);
 
   uint32_t qa[KS][4];
   float acc[MT][4];
@@ -603,7 +597,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     const bool last = me.tile + 1 == me.tiles || me.at + 1 >= count;
     if (last) {
       const bool whole = seg_tile0 == 0 && me.tile + 1 == me.tiles;
-      const int64_t part = id * 2 + (first_seg ? 0 : 1);
+      const int64_t part = int64_t(id) * 2 + (first_seg ? 0 : 1);
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (!whole && t == 0) {

@@ -182,62 +182,51 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // ------------------------------------------------ the run of this CTA
   const int P = bt.B * ar.most_r;
-  int64_t U = 0, u0 = 0, u1 = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t run = 0;
-    for (int p0 = 0; p0 < P; p0 += THREADS) {
-      const int p = p0 + int(threadIdx.x);
-      int64_t mine = 0;
-      if (p < P) {
-        Item it;
-        it.b = p / ar.most_r;
-        it.r = p - it.b * ar.most_r;
-        it.load(bt, c.tshift, ar.G, ROWS, pass ? nullptr : status);
-        if (it.valid()) mine = int64_t(it.tiles + START) * c.heads;
-      }
-      int64_t inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) sm.sum[warp] = inc;
-      __syncthreads();
-      int64_t before = run;
-      for (int w = 0; w < warp; ++w) before += sm.sum[w];
-      for (int w = 0; w < 13; ++w) run += sm.sum[w];
-      const int64_t first = before + inc - mine;
-      if (pass == 1) {
-        if (mine > 0 && u0 >= first && u0 < first + mine) {
-          sm.start_p = p;
-          sm.start_off = u0 - first;
-        }
-      }
-      __syncthreads();
-    }
-    if (pass == 0) {
-      U = run;
-      const int64_t W = workers(U, gridDim.x);
-      u0 = U && blockIdx.x < W ? run_start(blockIdx.x, U, W) : -1;
-      u1 = U && blockIdx.x < W ? run_start(blockIdx.x + 1, U, W) : -1;
-      if (U == 0) break;
-    }
+  auto units_at = [&](int p, int* st) {
+    if (p >= P) return int64_t(0);
+    Item it;
+    it.b = p / ar.most_r;
+    it.r = p - it.b * ar.most_r;
+    it.load(bt, c.tshift, ar.G, ROWS, st);
+    return it.valid() ? int64_t(it.tiles + START) * c.heads : int64_t(0);
+  };
+  const bool one = P <= THREADS;  // looked at once
+  int64_t U = 0, part = 0, first = 0, units = 0;
+  for (int p0 = 0; p0 < P; p0 += THREADS) {
+    units = units_at(p0 + int(threadIdx.x), status);
+    first = U + block_scan<13>(units, sm.sum, &part);
+    U += part;
   }
-  if (U == 0 || u0 < 0) {
-    if (threadIdx.x == 0) write_cut(ar.cuts + blockIdx.x, false, 0, 0, 0, 0, 0, 0, 0, 0, 0);
+  const Runs runs(U, gridDim.x);
+  if (int(blockIdx.x) >= runs.workers) {
+    if (threadIdx.x == 0) write_cut(ar.cuts + blockIdx.x, false, runs, 0, 0, 0, 0, 0, 0, 0);
     return;
   }
+  const int64_t u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
+  int64_t done = 0;
+  for (int p0 = 0; p0 < P; p0 += THREADS) {
+    if (!one) {
+      units = units_at(p0 + int(threadIdx.x), nullptr);
+      first = done + block_scan<13>(units, sm.sum, &part);
+      done += part;
+    }
+    if (units > 0 && u0 >= first && u0 < first + units) {
+      sm.start_p = p0 + int(threadIdx.x);
+      sm.start_off = u0 - first;
+    }
+  }
+  __syncthreads();
   Walk wk;
   wk.u0 = u0, wk.u1 = u1;
   wk.it.b = sm.start_p / ar.most_r;
   wk.it.r = sm.start_p - wk.it.b * ar.most_r;
   wk.it.load(bt, c.tshift, ar.G, ROWS, nullptr);
-  wk.it.h = int(sm.start_off / (wk.it.tiles + START));
+  wk.it.h = int(quotient(sm.start_off, wk.it.tiles + START));
   wk.begin = u0 - (sm.start_off - int64_t(wk.it.h) * (wk.it.tiles + START));
   wk.clip();
   if (threadIdx.x == 0)
-    write_cut(ar.cuts + blockIdx.x, wk.t0 > 0, wk.begin, wk.begin + START, wk.it.tiles, U,
-              workers(U, gridDim.x), wk.it.r, wk.it.n, wk.it.q0, wk.it.h);
+    write_cut(ar.cuts + blockIdx.x, wk.t0 > 0, runs, wk.begin, START, wk.it.tiles, wk.it.r,
+              wk.it.n, wk.it.q0, wk.it.h);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {

@@ -118,16 +118,52 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Units [u0, u1) of worker w: [w U / W, (w + 1) U / W).
-__device__ __forceinline__ int64_t run_start(int64_t w, int64_t U, int64_t W) { return w * U / W; }
-__device__ __forceinline__ int64_t run_owner(int64_t u, int64_t U, int64_t W) {
-  return ((u + 1) * W - 1) / U;
+// a / b for a >= 0, b > 0 (32-bit where both fit: a quarter of the instructions)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
-// Workers in use: no run is shorter than two units (a cut run costs a part in
-// the workspace, about a unit's bytes).
-__device__ __forceinline__ int64_t workers(int64_t U, int64_t W) {
-  const int64_t w = (U + 1) / 2;
-  return w < W ? w : W;
+
+// U units in equal runs for up to `most` workers: the first `rem` runs have
+// base + 1 units, the others base.  No run is shorter than two units (a cut run
+// costs a part in the workspace, about a unit's bytes).
+struct Runs {
+  int64_t base;
+  int workers, rem;
+  __device__ __forceinline__ Runs(int64_t U, int64_t most) {
+    const int64_t w = (U + 1) >> 1;
+    workers = int(w < most ? w : most);
+    base = workers ? quotient(U, workers) : 0;
+    rem = int(U - base * workers);
+  }
+  __device__ __forceinline__ int64_t start(int w) const { return w * base + min(w, rem); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    const int64_t longer = rem * (base + 1);
+    return u < longer ? int(quotient(u, base + 1)) : rem + int(quotient(u - longer, base));
+  }
+};
+
+// Exclusive prefix sum of `mine` over the block's threads (NW warps); *total gets
+// the sum.  Ends with a barrier of the block after `sums` has been read.
+template <int NW>
+__device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t* sums, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + inc - mine;
 }
 
 // ------------------------------------------------------------------- joining
@@ -140,15 +176,14 @@ struct __align__(16) Cut {
   int n, q0, h, pad;                          // of its sequence; kv head
 };
 
-// Written by one thread for each run, cutting or not.
-__device__ __forceinline__ void write_cut(Cut* cut, bool cuts, int64_t begin, int64_t first_unit,
-                                          int tiles, int64_t U, int64_t W, int rows, int n, int q0,
-                                          int h) {
+// Written by one thread for each run, cutting or not.  The segment's units are
+// `begin` and on, `extra` of them for its start and then `tiles`.
+__device__ __forceinline__ void write_cut(Cut* cut, bool cuts, const Runs& runs, int64_t begin,
+                                          int extra, int tiles, int rows, int n, int q0, int h) {
   int4 a = make_int4(-1, 0, 0, 0), b = make_int4(0, 0, 0, 0);
   if (cuts) {
-    const int64_t wa = run_owner(first_unit, U, W);
-    a = make_int4(int(wa), int(run_owner(first_unit + tiles - 1, U, W)),
-                  run_start(wa, U, W) < begin ? 1 : 0, rows);
+    const int wa = runs.owner(begin + extra);
+    a = make_int4(wa, runs.owner(begin + extra + tiles - 1), runs.start(wa) < begin ? 1 : 0, rows);
     b = make_int4(n, q0, h, 0);
   }
   reinterpret_cast<int4*>(cut)[0] = a;
