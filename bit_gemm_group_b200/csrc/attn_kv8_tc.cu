@@ -89,6 +89,15 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t& a, uint32_t& b) {
   }
 }
 
+__device__ __forceinline__ uint64_t u32x2(uint32_t a, uint32_t b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  return u32x2(__float_as_uint(a), __float_as_uint(b));
+}
+
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -273,7 +282,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool live = rr < it.n * ar.G;
       const int i = live ? rr / ar.G : 0;
       const int pos = it.len - it.n + i;
-      const int lim = live ? min(it.len, pos + 1) : 0;
+      // (a row of no query takes part as zeros, and asks for no masking)
+      const int lim = live ? min(it.len, pos + 1) : 0x7fffffff;
       // -------- this row of queries, as f16 in the swizzled operand layout
       float fq;
       {
@@ -334,28 +344,47 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after_sync();
         const int tok0 = (wk.t0 + j) * TK;
         const float4* scl = sm.scale[b & 3];
-        // -------- the row's maximum
+        // -------- weights against the maximum so far; where a score is more than
+        // LAG above it the maximum moves and they are computed again
         const bool edge = __any_sync(0xffffffffu, tok0 + TK > lim);
-        float mx = -CUDART_INF_F;
+        uint32_t p[64];
+        float sum;
+        while (true) {
+          const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+          float mx = -CUDART_INF_F;
+          sum = 0.f;
+          uint32_t s[2][16];
+          tc::tmem_ld_x16(st, s[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tc::tmem_ld_x32(st + q * 32, s);
-          tc::tmem_wait_ld();
-          if (edge)
+          for (int q = 0; q < 8; ++q) {  // 16 positions, of one page
+            const float4 f = scl[q];
+            tc::tmem_wait_ld();
+            if (q < 7) tc::tmem_ld_x16(st + (q + 1) * 16, s[(q + 1) & 1]);
+            uint32_t(&v)[16] = s[q & 1];
+            if (edge)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (tok0 + q * 32 + e >= lim) s[e] = 0xFF800000u;
+              for (int e = 0; e < 16; ++e)
+                if (tok0 + q * 16 + e >= lim) v[e] = 0xFF800000u;
+            const float mul = fmaxf(fq * f.x, 1e-37f);
+            float a = __uint_as_float(v[0]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 f = scl[2 * q + k];
-            float a = __uint_as_float(s[16 * k]);
+            for (int e = 1; e < 16; ++e) a = fmaxf(a, __uint_as_float(v[e]));
+            mx = fmaxf(mx, fmaf(a, mul, f.y));
+            const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(f.y + off, f.y + off);
+            uint64_t part = 0;
 #pragma unroll
-            for (int e = 1; e < 16; ++e) a = fmaxf(a, __uint_as_float(s[16 * k + e]));
-            mx = fmaxf(mx, a == -CUDART_INF_F ? a : fmaf(a, fq * f.x, f.y));
+            for (int e = 0; e < 8; ++e) {
+              uint64_t t = u32x2(v[2 * e], v[2 * e + 1]);
+              asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(t) : "l"(mul2), "l"(add2));
+              const float x0 = exp2_approx(__uint_as_float(uint32_t(t)));
+              const float x1 = exp2_approx(__uint_as_float(uint32_t(t >> 32)));
+              const uint64_t y = f32x2(x0, x1);
+              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part) : "l"(y));
+              p[q * 8 + e] = f16x2(x0, x1);
+            }
+            sum = fmaf(__uint_as_float(uint32_t(part)) + __uint_as_float(uint32_t(part >> 32)), f.z, sum);
           }
-        }
-        if (__any_sync(0xffffffffu, mx > m + LAG)) {
+          if (!__any_sync(0xffffffffu, mx > m + LAG)) break;
           const float now = fmaxf(m, mx);
           const float al = now == m ? 1.f : exp2_approx(m - now);
           m = now;
@@ -375,33 +404,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        // -------- weights
-        const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+        if (!ok) break;
+        l += sum;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tc::tmem_ld_x32(st + q * 32, s);
-          tc::tmem_wait_ld();
-          if (edge)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (tok0 + q * 32 + e >= lim) s[e] = 0xFF800000u;
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 f = scl[2 * q + k];
-            const float mul = fq * f.x, add = f.y + off;
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = exp2_approx(fmaf(__uint_as_float(s[16 * k + 2 * e]), mul, add));
-              const float b = exp2_approx(fmaf(__uint_as_float(s[16 * k + 2 * e + 1]), mul, add));
-              sum += a + b;
-              p[8 * k + e] = f16x2(a, b);
-            }
-            l = fmaf(sum, f.z, l);
-          }
-          tc::tmem_st_x16(st + q * 16, p);
+          uint32_t(&v)[16] = *reinterpret_cast<uint32_t(*)[16]>(&p[q * 16]);
+          tc::tmem_st_x16(st + q * 16, v);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -510,34 +518,35 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS)) {
       const Item& it = wk.it;
       const int J = wk.t1 - wk.t0;
-      // page of each 16 positions of a block: lane g of a warp looks up group
-      // g, and in the first warp its scales
-      int page;
-      float ks, vs;
-      auto look_up = [&](int j) {
+      // Lane g of a warp looks after positions 16 g to 16 g + 15 of a block (one
+      // page): table entry two blocks ahead, address and (first warp) scales one
+      // block ahead, so that nothing here waits for the load before it.
+      auto entry = [&](int j) {
         const int tok = (wk.t0 + j) * TK + lane * 16;
-        page = -1, ks = 1.f, vs = -1.f;
-        if (lane < 8 && j < J && tok < it.len) {
-          page = __ldg(bt.table + int64_t(it.b) * bt.width + (tok >> c.tshift));
-          if (page < 0 || page >= c.pages) {
-            record_error(status, WQ_ERR_ARG);
-            page = -1;
-          } else if (warp == 8) {
-            ks = fmaxf(__ldg(c.ks + c.block(page, it.h)), 1e-30f);
-            vs = fmaxf(__ldg(c.vs + c.block(page, it.h)), 1e-30f);
-          }
-        }
+        return lane < 8 && j < J && tok < it.len
+                   ? __ldg(bt.table + int64_t(it.b) * bt.width + (tok >> c.tshift))
+                   : -2;
       };
-      auto load = [&](uint4 (&w)[N], const uint8_t* src, int j, int pages) {
+      auto from = [&](int page, int j) {  // of the group's first code, -1 where it has no page
+        if (page < 0 || page >= c.pages) {
+          if (page != -2) record_error(status, WQ_ERR_ARG);
+          return int64_t(-1);
+        }
+        return ((c.block(page, it.h) << c.tshift) + (((wk.t0 + j) * TK + lane * 16) & (T_ - 1))) * D;
+      };
+      auto load = [&](uint4 (&w)[N], const uint8_t* src, int j, int64_t at, bool full) {
+        const uint8_t* mine = src + (tr & 15) * D + piece * 16;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int r = tr + i * STEP, tok = (wk.t0 + j) * TK + r;
-          const int pg = __shfl_sync(0xffffffffu, pages, r >> 4);
+          const int r = tr + i * STEP;
+          const int64_t o = __shfl_sync(0xffffffffu, at, r >> 4);
           w[i] = make_uint4(0, 0, 0, 0);
-          if (pg >= 0 && tok < it.len)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(
-                src + ((c.block(pg, it.h) << c.tshift) + (tok & (T_ - 1))) * D + piece * 16));
+          if (full || (o >= 0 && (wk.t0 + j) * TK + r < it.len))
+            w[i] = __ldg(reinterpret_cast<const uint4*>(mine + o));
         }
+      };
+      auto is_full = [&](int j, int64_t at) {
+        return (wk.t0 + j + 1) * TK <= it.len && __all_sync(0xffffffffu, lane >= 8 || at >= 0);
       };
       auto store = [&](const uint4 (&w)[N], uint32_t dst) {
 #pragma unroll
@@ -562,25 +571,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       };
       uint4 kw[N], vw[N];
-      look_up(0);
-      load(kw, c.kq, 0, page);
+      int64_t at = from(entry(0), 0);
+      int next = entry(1);
+      bool full = is_full(0, at);
+      float ks = 1.f, vs = -1.f;
+      auto scales_at = [&](int64_t a) {
+        if (warp == 8 && a >= 0) {
+          const int64_t blk = (a / D) >> c.tshift;
+          ks = __ldg(c.ks + blk), vs = __ldg(c.vs + blk);
+        } else {
+          ks = 1.f, vs = -1.f;
+        }
+      };
+      scales_at(at);
+      load(kw, c.kq, 0, at, full);
       for (int j = 0; j < J; ++j, ++block) {
         const uint32_t s = block & 1u, turn = ((block >> 1) & 1u) ^ 1u;
         // one operand's codes are on their way while the other's are expanded
-        load(vw, c.vq, j, page);
-        const float4 scales =
-            make_float4(ks, vs < 0.f ? -CUDART_INF_F : __log2f(vs), vs < 0.f ? 0.f : __fdividef(1.f, vs), 0.f);
-        look_up(j + 1);
+        load(vw, c.vq, j, at, full);
+        const float ks_now = ks, vs_now = vs;
+        const int after = entry(j + 2);
+        at = from(next, j + 1);
+        scales_at(at);
+        next = after;
+        full = is_full(j + 1, at);
         ok = tc::wait_warp(&sm.kempty[s], turn, wd);
         if (!ok) break;
         if (warp == 8) {
-          if (lane < 8) sm.scale[block & 3][lane] = scales;
+          const float v = fmaxf(vs_now, 1e-30f);
+          if (lane < 8)
+            sm.scale[block & 3][lane] =
+                make_float4(fmaxf(ks_now, 1e-30f), vs_now < 0.f ? -CUDART_INF_F : __log2f(v),
+                            vs_now < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sm.scfull[block & 3]);
         }
         store(kw, ksm + s * S::TILE);
         if (lane == 0) tc::mbar_arrive(&sm.kfull[s]);
-        if (j + 1 < J) load(kw, c.kq, j + 1, page);
+        if (j + 1 < J) load(kw, c.kq, j + 1, at, full);
         ok = tc::wait_warp(&sm.vempty[s], turn, wd);
         if (!ok) break;
         store(vw, vsm + s * S::TILE);
@@ -590,54 +618,67 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!ok) sm.abort_flag = 1;
   } else {
     // ------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
-      uint32_t block = 0, seg = 0, opx[2] = {0, 0};
-      bool ok = true;
-      for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
-        const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
-        ok = tc::wait_bounded(&sm.qfull, seg & 1u, wd);
+    // (the whole warp walks the loop and one lane issues, so that operand
+    // addresses stay in uniform registers)
+    constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
+    uint32_t block = 0, seg = 0, opx0 = 0, opx1 = 0;
+    bool ok = true;
+    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
+      const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
+      ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
+      tc::fence_after_sync();
+      // scores of round k: tile k & 1, block k / 2 (PAIR) or k
+      auto scores = [&](int k) {
+        const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
+        if (!tc::wait_warp(&sm.kfull[s], (b >> 1) & 1u, wd)) return false;
         tc::fence_after_sync();
-        // scores of round k: tile k & 1, block k / 2 (PAIR) or k
-        auto scores = [&](int k) {
-          const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
-          if (!tc::wait_bounded(&sm.kfull[s], (b >> 1) & 1u, wd)) return false;
-          tc::fence_after_sync();
-          const uint32_t kb = ksm + s * S::TILE, qb = qs + (PAIR ? x * S::TILE : 0);
+        const uint64_t dk = tc::sdesc_k_sw128(ksm + s * S::TILE);
+        const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
+        if (tc::elect_one()) {
 #pragma unroll
           for (int term = 0; term < (TWO ? 2 : 1); ++term)
 #pragma unroll
             for (int k16 = 0; k16 < D / 16; ++k16) {
-              const uint32_t at = (k16 / 4) * PLANE + (k16 & 3) * 32;
-              tc::mma_f16_ss(tmem + x * 128, tc::sdesc_k_sw128(qb + term * S::TILE + at),
-                             tc::sdesc_k_sw128(kb + at), idesc_s, (term | k16) != 0);
+              const uint32_t at = ((k16 / 4) * PLANE + (k16 & 3) * 32) >> 4;
+              tc::mma_f16_ss(tmem + x * 128, dq + uint64_t(term * (S::TILE >> 4) + at),
+                             dk + uint64_t(at), idesc_s, (term | k16) != 0);
             }
           tc::mma_commit(&sm.sfull[x]);
           if (!PAIR || x == 1) tc::mma_commit(&sm.kempty[s]);
-          return true;
-        };
-        for (int k = 0; k < 2 && k < N && ok; ++k) ok = scores(k);
-        for (int k = 0; k < N && ok; ++k) {
-          const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
-          if (!(ok = tc::wait_bounded(&sm.vfull[s], (b >> 1) & 1u, wd))) break;
-          if (!(ok = tc::wait_bounded(&sm.pfull[x], opx[x] & 1u, wd))) break;
-          ++opx[x];
-          tc::fence_after_sync();
-          const uint32_t vb = vsm + s * S::TILE;
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int k = 0; k < 2 && k < N && ok; ++k) ok = scores(k);
+      for (int k = 0; k < N && ok; ++k) {
+        const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
+        if (!(ok = tc::wait_warp(&sm.vfull[s], (b >> 1) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.pfull[x], (x ? opx1 : opx0) & 1u, wd))) break;
+        if (x)
+          ++opx1;
+        else
+          ++opx0;
+        tc::fence_after_sync();
+        const uint64_t dv = sdesc_mn_sw128(vsm + s * S::TILE, PLANE);
+        if (tc::elect_one()) {
 #pragma unroll
           for (int k16 = 0; k16 < TK / 16; ++k16)
-            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + k16 * 8,
-                           sdesc_mn_sw128(vb + k16 * 2048, PLANE), idesc_o, k > 1 || k16 != 0);
+            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + k16 * 8, dv + uint64_t(k16 * 128),
+                           idesc_o, k > 1 || k16 != 0);
           tc::mma_commit(&sm.odone[x]);
           if (!PAIR || x == 1) tc::mma_commit(&sm.vempty[s]);
-          if (k + 2 < N) ok = scores(k + 2);
         }
-        block += J;
+        __syncwarp();
+        if (k + 2 < N) ok = scores(k + 2);
       }
-      if (!ok) sm.abort_flag = 1;
+      block += J;
+    }
+    if (!ok) sm.abort_flag = 1;
+    if (tc::elect_one()) {
       tc::mma_commit(&sm.drain);
       tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
+    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
