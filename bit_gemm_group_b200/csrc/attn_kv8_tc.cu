@@ -2,7 +2,7 @@
 // rows to a (sequence, kv head): prompts, chunks of prompts, drafts.
 //
 // The mathematics of attn_kv8.cu on the fifth-generation tensor cores.  One CTA
-// per SM of 13 warps; 128 rows (query, head) are one tensor-core tile:
+// per SM; 128 rows (query, head) are one tensor-core tile:
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a row per thread: scores
 //                   from tensor memory, weights back to it as f16
 //   warps 8-11      converters: 128 positions of codes at a time from the pages
@@ -38,7 +38,11 @@ namespace wq {
 namespace kv8 {
 namespace tcore {
 
-constexpr int THREADS = 13 * 32;
+// 16 warps of 128 registers at launch; the softmax keeps a block's 64 words of
+// weights and takes 160, the converters 112, the issuer's four warps 80
+constexpr int WARPS = 16, THREADS = WARPS * 32;
+constexpr int REGS_SOFTMAX = 160, REGS_CONVERT = 112, REGS_ISSUE = 80;
+static_assert(2 * REGS_SOFTMAX + REGS_CONVERT + REGS_ISSUE <= 4 * 128, "registers");
 constexpr int TK = 128;    // positions per block
 constexpr int START = 2;   // units an item's queries and results count
 
@@ -51,7 +55,7 @@ struct Smem {
     uint64_t sfull[2], pfull[2], odone[2], scfull[4], mfull, mfree, drain;
     float4 scale[4][8];     // per block in flight and 16 positions: ks, log2 vs, 1 / vs
     float m[128], l[128];   // of tile 1, where both tiles are the same rows
-    int64_t sum[13], start_off;
+    int64_t sum[WARPS], start_off;
     int start_p, tmem_base, abort_flag;
   };
   static constexpr size_t BYTES = 1024 + BLOCKS + sizeof(Ctrl);
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   int64_t U = 0, part = 0, first = 0, units = 0;
   for (int p0 = 0; p0 < P; p0 += THREADS) {
     units = units_at(p0 + int(threadIdx.x), status);
-    first = U + block_scan<13>(units, sm.sum, &part);
+    first = U + block_scan<WARPS>(units, sm.sum, &part);
     U += part;
   }
   const Runs runs(U, gridDim.x);
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int p0 = 0; p0 < P; p0 += THREADS) {
     if (!one) {
       units = units_at(p0 + int(threadIdx.x), nullptr);
-      first = done + block_scan<13>(units, sm.sum, &part);
+      first = done + block_scan<WARPS>(units, sm.sum, &part);
       done += part;
     }
     if (units > 0 && u0 >= first && u0 < first + units) {
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int x = warp >> 2;                       // tile
     const int row = (warp & 3) * 32 + lane;        // of the tile
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -507,6 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!ok) sm.abort_flag = 1;
   } else if (warp < 12) {
     // ------------------------------------------------------------- converters
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONVERT));
     // a thread's pieces: 16 codes of rows tr, tr + STEP, ... of the block
     constexpr int PER = D / 16, STEP = 128 / PER, N = 128 / STEP;  // N pieces of K and of V
     const int ct = int(threadIdx.x) - 256, piece = ct % PER, tr = ct / PER;
@@ -620,9 +626,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------- MMA issuer
     // (the whole warp walks the loop and one lane issues, so that operand
     // addresses stay in uniform registers)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
     constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
     uint32_t block = 0, seg = 0, opx0 = 0, opx1 = 0;
-    bool ok = true;
+    bool ok = warp == 12;
     for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
       const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
@@ -673,8 +680,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       block += J;
     }
-    if (!ok) sm.abort_flag = 1;
-    if (tc::elect_one()) {
+    if (!ok && warp == 12) sm.abort_flag = 1;
+    if (warp == 12 && tc::elect_one()) {
       tc::mma_commit(&sm.drain);
       tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
