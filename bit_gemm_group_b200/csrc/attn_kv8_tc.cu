@@ -5,11 +5,11 @@
 // per SM; 128 rows (query, head) are one tensor-core tile:
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a row per thread: scores
 //                   from tensor memory, weights back to it as f16
-//   warps 8-11      converters: 128 positions of codes at a time from the pages
-//                   to f16 (exactly) in shared memory, keys and values in the
-//                   same 128-byte swizzled layout (values are the product's
-//                   K operand along their rows: MN-major)
-//   warp 12         issues tcgen05.mma kind::f16: scores Q K^T (both operands
+//   warps 8-11      converters of keys: 128 positions of codes at a time from the
+//                   pages to f16 (exactly) in shared memory
+//   warps 12-15     converters of values, into the same 128-byte swizzled layout
+//                   (the product's sum runs along their rows: MN-major)
+//   warp 16         issues tcgen05.mma kind::f16: scores Q K^T (both operands
 //                   in shared memory), then weights (tensor memory) times V
 //
 // PAIR: the two tiles are 256 rows of one (sequence, head) and share every
@@ -38,11 +38,11 @@ namespace wq {
 namespace kv8 {
 namespace tcore {
 
-// 16 warps of 128 registers at launch; the softmax keeps a block's 64 words of
-// weights and takes 160, the converters 112, the issuer's four warps 80
-constexpr int WARPS = 16, THREADS = WARPS * 32;
-constexpr int REGS_SOFTMAX = 160, REGS_CONVERT = 112, REGS_ISSUE = 80;
-static_assert(2 * REGS_SOFTMAX + REGS_CONVERT + REGS_ISSUE <= 4 * 128, "registers");
+// 20 warps of 96 registers at launch; the softmax keeps a block's 64 words of
+// weights and takes 136, the converters 80, the issuer's four warps 48
+constexpr int WARPS = 20, THREADS = WARPS * 32;
+constexpr int REGS_SOFTMAX = 136, REGS_CONVERT = 80, REGS_ISSUE = 48;
+static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * 96, "registers");
 constexpr int TK = 128;    // positions per block
 constexpr int START = 2;   // units an item's queries and results count
 
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     sm.abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tc::tmem_alloc(reinterpret_cast<uint32_t*>(&sm.tmem_base), 512);
     tc::tmem_relinquish();
   }
@@ -510,12 +510,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       block += J;
     }
     if (!ok) sm.abort_flag = 1;
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ------------------------------------------------------------- converters
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONVERT));
     // a thread's pieces: 16 codes of rows tr, tr + STEP, ... of the block
-    constexpr int PER = D / 16, STEP = 128 / PER, N = 128 / STEP;  // N pieces of K and of V
-    const int ct = int(threadIdx.x) - 256, piece = ct % PER, tr = ct / PER;
+    constexpr int PER = D / 16, STEP = 128 / PER, N = 128 / STEP;  // N pieces of a block
+    const bool values = warp >= 12;
+    const uint8_t* src = values ? c.vq : c.kq;
+    const uint32_t region = values ? vsm : ksm;
+    uint64_t* const full = values ? sm.vfull : sm.kfull;
+    uint64_t* const empty = values ? sm.vempty : sm.kempty;
+    const int ct = int(threadIdx.x) & 127, piece = ct % PER, tr = ct / PER;
     // a piece is two 16-byte parts of a row of 64 f16; lanes of the upper
     // half planes store them in the other order (bank conflicts)
     const int plane = piece / 4, part0 = (piece & 3) * 2, swap = plane & 1;
@@ -540,21 +545,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         return ((c.block(page, it.h) << c.tshift) + (((wk.t0 + j) * TK + lane * 16) & (T_ - 1))) * D;
       };
-      auto load = [&](uint4 (&w)[N], const uint8_t* src, int j, int64_t at, bool full) {
+      uint4 w[N];
+      auto load = [&](int j, int64_t at, bool whole) {
         const uint8_t* mine = src + (tr & 15) * D + piece * 16;
+        if (whole) {
+          int64_t o[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = tr + i * STEP;
-          const int64_t o = __shfl_sync(0xffffffffu, at, r >> 4);
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (full || (o >= 0 && (wk.t0 + j) * TK + r < it.len))
-            w[i] = __ldg(reinterpret_cast<const uint4*>(mine + o));
+          for (int i = 0; i < N; ++i) o[i] = __shfl_sync(0xffffffffu, at, (tr + i * STEP) >> 4);
+#pragma unroll
+          for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(mine + o[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = tr + i * STEP;
+            const int64_t o = __shfl_sync(0xffffffffu, at, r >> 4);
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (o >= 0 && (wk.t0 + j) * TK + r < it.len)
+              w[i] = __ldg(reinterpret_cast<const uint4*>(mine + o));
+          }
         }
       };
       auto is_full = [&](int j, int64_t at) {
         return (wk.t0 + j + 1) * TK <= it.len && __all_sync(0xffffffffu, lane >= 8 || at >= 0);
       };
-      auto store = [&](const uint4 (&w)[N], uint32_t dst) {
+      auto store = [&](uint32_t dst) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int r = tr + i * STEP;
@@ -576,10 +590,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       };
-      uint4 kw[N], vw[N];
       int64_t at = from(entry(0), 0);
       int next = entry(1);
-      bool full = is_full(0, at);
       float ks = 1.f, vs = -1.f;
       auto scales_at = [&](int64_t a) {
         if (warp == 8 && a >= 0) {
@@ -590,18 +602,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       scales_at(at);
-      load(kw, c.kq, 0, at, full);
+      load(0, at, is_full(0, at));
       for (int j = 0; j < J; ++j, ++block) {
-        const uint32_t s = block & 1u, turn = ((block >> 1) & 1u) ^ 1u;
-        // one operand's codes are on their way while the other's are expanded
-        load(vw, c.vq, j, at, full);
+        const uint32_t s = block & 1u;
         const float ks_now = ks, vs_now = vs;
         const int after = entry(j + 2);
         at = from(next, j + 1);
         scales_at(at);
         next = after;
-        full = is_full(j + 1, at);
-        ok = tc::wait_warp(&sm.kempty[s], turn, wd);
+        const bool whole = is_full(j + 1, at);
+        ok = tc::wait_warp(&empty[s], ((block >> 1) & 1u) ^ 1u, wd);
         if (!ok) break;
         if (warp == 8) {
           const float v = fmaxf(vs_now, 1e-30f);
@@ -612,13 +622,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sm.scfull[block & 3]);
         }
-        store(kw, ksm + s * S::TILE);
-        if (lane == 0) tc::mbar_arrive(&sm.kfull[s]);
-        if (j + 1 < J) load(kw, c.kq, j + 1, at, full);
-        ok = tc::wait_warp(&sm.vempty[s], turn, wd);
-        if (!ok) break;
-        store(vw, vsm + s * S::TILE);
-        if (lane == 0) tc::mbar_arrive(&sm.vfull[s]);
+        store(region + s * S::TILE);
+        // (before the next loads: a release waits for loads on their way)
+        if (lane == 0) tc::mbar_arrive(&full[s]);
+        if (j + 1 < J) load(j + 1, at, whole);
       }
     }
     if (!ok) sm.abort_flag = 1;
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
     constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
     uint32_t block = 0, seg = 0, opx0 = 0, opx1 = 0;
-    bool ok = warp == 12;
+    bool ok = warp == 16;
     for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
       const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
@@ -680,8 +687,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       block += J;
     }
-    if (!ok && warp == 12) sm.abort_flag = 1;
-    if (warp == 12 && tc::elect_one()) {
+    if (!ok && warp == 16) sm.abort_flag = 1;
+    if (warp == 16 && tc::elect_one()) {
       tc::mma_commit(&sm.drain);
       tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
@@ -689,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
