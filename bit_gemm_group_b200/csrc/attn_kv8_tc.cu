@@ -9,7 +9,7 @@
 //                   pages to f16 (exactly) in shared memory
 //   warps 12-15     converters of values, into the same 128-byte swizzled layout
 //                   (the product's sum runs along their rows: MN-major)
-//   warp 16         issues tcgen05.mma kind::f16: scores Q K^T (both operands
+//   warps 16, 17    issue, a warp per tile, tcgen05.mma kind::f16: scores Q K^T (both operands
 //                   in shared memory), then weights (tensor memory) times V
 //
 // PAIR: the two tiles are 256 rows of one (sequence, head) and share every
@@ -43,17 +43,26 @@ namespace tcore {
 constexpr int WARPS = 20, THREADS = WARPS * 32;
 constexpr int REGS_SOFTMAX = 136, REGS_CONVERT = 80, REGS_ISSUE = 48;
 static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * 96, "registers");
-constexpr int TK = 128;    // positions per block
-constexpr int START = 2;   // units an item's queries and results count
+constexpr int TK = 64;      // positions per block
+constexpr int STAGES = 4;   // blocks of keys and of values in shared memory
+constexpr int SCALES = 8;   // blocks whose scales are kept
+constexpr int START = 4;    // units an item's queries and results count
 
 template <int D>
 struct Smem {
   static constexpr int TILE = 128 * D * 2;  // 128 rows of f16
-  static constexpr int BLOCKS = 6 * TILE;   // Q 2, K 2, V 2
+  static constexpr int BLOCK = TK * D * 2;
+  static constexpr int BLOCKS = 2 * TILE + 2 * STAGES * BLOCK;  // Q 2, K, V
   struct Ctrl {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], qfull;
-    uint64_t sfull[2], pfull[2], odone[2], scfull[4], mfull, mfree, drain;
-    float4 scale[4][8];     // per block in flight and 16 positions: ks, log2 vs, 1 / vs
+    uint64_t kfull[STAGES], kempty[STAGES], vfull[STAGES], vempty[STAGES], qfull;
+    // per tile: two rounds in turn (a wait tells a round from the one two before,
+    // which is known to be over, but not from the one in between)
+    uint64_t sfull[2][2], pfull[2][2], odone[2][2];
+    uint64_t scfull[SCALES], mfull, mfree, drain[2];
+    // per block and 16 positions: ks, log2 vs, 1 / vs.  A slot is written again 8
+    // blocks later, when the scores 4 blocks later are done, whose predecessors 2
+    // blocks back have been through the softmax.
+    float4 scale[SCALES][TK / 16];
     float m[128], l[128];   // of tile 1, where both tiles are the same rows
     int64_t sum[WARPS], start_off;
     int start_p, tmem_base, abort_flag;
@@ -182,12 +191,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   using S = Smem<D>;
   constexpr int ROWS = PAIR ? 256 : 128;
   constexpr bool TWO = !PAIR && std::is_same<TQ, __half>::value;  // queries in two terms
-  constexpr int PLANE = 128 * 128;  // 128 rows of 64 f16
+  constexpr int PLANE = 128 * 128, KVPLANE = TK * 128;  // 128 (64) rows of 64 f16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   auto& sm = *reinterpret_cast<typename S::Ctrl*>(base + S::BLOCKS);
-  const uint32_t qs = tc::smem_u32(base), ksm = qs + 2 * S::TILE, vsm = ksm + 2 * S::TILE;
+  const uint32_t qs = tc::smem_u32(base), ksm = qs + 2 * S::TILE, vsm = ksm + STAGES * S::BLOCK;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,20 +251,24 @@ __global__ void __launch_bounds__(THREADS, 1)
               wk.it.n, wk.it.q0, wk.it.h);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       tc::mbar_init(&sm.kfull[i], 4);
       tc::mbar_init(&sm.vfull[i], 4);
-      tc::mbar_init(&sm.kempty[i], 1);
-      tc::mbar_init(&sm.vempty[i], 1);
-      tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.pfull[i], 4);
-      tc::mbar_init(&sm.odone[i], 1);
+      tc::mbar_init(&sm.kempty[i], PAIR ? 2 : 1);
+      tc::mbar_init(&sm.vempty[i], PAIR ? 2 : 1);
     }
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&sm.scfull[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 2; ++k) {
+        tc::mbar_init(&sm.sfull[i][k], 1);
+        tc::mbar_init(&sm.pfull[i][k], 4);
+        tc::mbar_init(&sm.odone[i][k], 1);
+      }
+      tc::mbar_init(&sm.drain[i], 1);
+    }
+    for (int i = 0; i < SCALES; ++i) tc::mbar_init(&sm.scfull[i], 1);
     tc::mbar_init(&sm.mfull, 4);
     tc::mbar_init(&sm.mfree, 4);
     tc::mbar_init(&sm.qfull, 8);
-    tc::mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     tc::fence_mbar_init();
   }
@@ -276,7 +289,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int x = warp >> 2;                       // tile
     const int row = (warp & 3) * 32 + lane;        // of the tile
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t st = tmem + lanes + uint32_t(x) * 128;        // scores, weights
+    // scores, and weights over them: two buffers of 64 columns, taken in turn
+    const uint32_t st0 = tmem + lanes + uint32_t(x) * 128;
     const uint32_t ot = tmem + lanes + 256 + uint32_t(x) * 128;  // result
     uint32_t op = 0;  // tensor-core rounds of this tile so far
     bool ok = true, first_seg = true;
@@ -343,16 +357,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       int done = 0;  // of this tile in this segment
       for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
         const uint32_t b = block + uint32_t(j);
-        if (!(ok = tc::wait_warp(&sm.sfull[x], op & 1u, wd) &&
-                   tc::wait_warp(&sm.scfull[b & 3], (b >> 2) & 1u, wd)))
+        const uint32_t buf = op & 1u, st = st0 + buf * TK;
+        if (!(ok = tc::wait_warp(&sm.sfull[x][buf], (op >> 1) & 1u, wd) &&
+                   tc::wait_warp(&sm.scfull[b % SCALES], (b / SCALES) & 1u, wd)))
           break;
         tc::fence_after_sync();
         const int tok0 = (wk.t0 + j) * TK;
-        const float4* scl = sm.scale[b & 3];
+        const float4* scl = sm.scale[b % SCALES];
         // -------- weights against the maximum so far; where a score is more than
         // LAG above it the maximum moves and they are computed again
         const bool edge = __any_sync(0xffffffffu, tok0 + TK > lim);
-        uint32_t p[64];
+        uint32_t p[TK / 2];
         float sum;
         while (true) {
           const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
@@ -361,10 +376,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t s[2][16];
           tc::tmem_ld_x16(st, s[0]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {  // 16 positions, of one page
+          for (int q = 0; q < TK / 16; ++q) {  // 16 positions, of one page
             const float4 f = scl[q];
             tc::tmem_wait_ld();
-            if (q < 7) tc::tmem_ld_x16(st + (q + 1) * 16, s[(q + 1) & 1]);
+            if (q + 1 < TK / 16) tc::tmem_ld_x16(st + (q + 1) * 16, s[(q + 1) & 1]);
             uint32_t(&v)[16] = s[q & 1];
             if (edge)
 #pragma unroll
@@ -396,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           l *= al;
           if (done) {
             // the products that add to the result so far are complete
-            if (!(ok = tc::wait_warp(&sm.odone[x], (op - 1) & 1u, wd))) break;
+            if (!(ok = tc::wait_warp(&sm.odone[x][(op - 1) & 1u], ((op - 1) >> 1) & 1u, wd))) break;
             tc::fence_after_sync();
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -412,18 +427,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         l += sum;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < TK / 32; ++q) {
           uint32_t(&v)[16] = *reinterpret_cast<uint32_t(*)[16]>(&p[q * 16]);
           tc::tmem_st_x16(st + q * 16, v);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.pfull[x]);
+        if (lane == 0) tc::mbar_arrive_relaxed(&sm.pfull[x][buf]);
       }
       if (!ok) break;
       if (done) {
-        if (!(ok = tc::wait_warp(&sm.odone[x], (op - 1) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.odone[x][(op - 1) & 1u], ((op - 1) >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
       }
       // -------- results
@@ -514,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------- converters
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONVERT));
     // a thread's pieces: 16 codes of rows tr, tr + STEP, ... of the block
-    constexpr int PER = D / 16, STEP = 128 / PER, N = 128 / STEP;  // N pieces of a block
+    constexpr int PER = D / 16, STEP = 128 / PER, N = TK / STEP;  // N pieces of a block
     const bool values = warp >= 12;
     const uint8_t* src = values ? c.vq : c.kq;
     const uint32_t region = values ? vsm : ksm;
@@ -534,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // block ahead, so that nothing here waits for the load before it.
       auto entry = [&](int j) {
         const int tok = (wk.t0 + j) * TK + lane * 16;
-        return lane < 8 && j < J && tok < it.len
+        return lane < TK / 16 && j < J && tok < it.len
                    ? __ldg(bt.table + int64_t(it.b) * bt.width + (tok >> c.tshift))
                    : -2;
       };
@@ -545,8 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         return ((c.block(page, it.h) << c.tshift) + (((wk.t0 + j) * TK + lane * 16) & (T_ - 1))) * D;
       };
-      uint4 w[N];
-      auto load = [&](int j, int64_t at, bool whole) {
+      auto load = [&](uint4 (&w)[N], int j, int64_t at, bool whole) {
         const uint8_t* mine = src + (tr & 15) * D + piece * 16;
         if (whole) {
           int64_t o[N];
@@ -566,9 +580,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       auto is_full = [&](int j, int64_t at) {
-        return (wk.t0 + j + 1) * TK <= it.len && __all_sync(0xffffffffu, lane >= 8 || at >= 0);
+        return (wk.t0 + j + 1) * TK <= it.len && __all_sync(0xffffffffu, lane >= TK / 16 || at >= 0);
       };
-      auto store = [&](uint32_t dst) {
+      auto store = [&](const uint4 (&w)[N], uint32_t dst) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int r = tr + i * STEP;
@@ -577,7 +591,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           expand<FMT>(w[i].y, h[2], h[3]);
           expand<FMT>(w[i].z, h[4], h[5]);
           expand<FMT>(w[i].w, h[6], h[7]);
-          const uint32_t p0 = dst + plane * PLANE + r * 128 + ((part0 ^ (r & 7)) << 4);
+          const uint32_t p0 = dst + plane * KVPLANE + r * 128 + ((part0 ^ (r & 7)) << 4);
           const uint32_t p1 = p0 ^ 16;
           if (swap) {
             sts128(p1, h[4], h[5], h[6], h[7]);
@@ -590,42 +604,42 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       };
-      int64_t at = from(entry(0), 0);
-      int next = entry(1);
-      float ks = 1.f, vs = -1.f;
-      auto scales_at = [&](int64_t a) {
-        if (warp == 8 && a >= 0) {
-          const int64_t blk = (a / D) >> c.tshift;
+      // the codes of two blocks are on their way (or a block's being expanded)
+      uint4 w0[N], w1[N];
+      float ks0 = 1.f, vs0 = -1.f, ks1 = 1.f, vs1 = -1.f;
+      int next = entry(0);
+      auto fetch = [&](uint4 (&w)[N], float& ks, float& vs, int j) {
+        const int64_t at = from(next, j);
+        next = entry(j + 1);
+        ks = 1.f, vs = -1.f;
+        if (warp == 8 && at >= 0) {
+          const int64_t blk = (at / D) >> c.tshift;
           ks = __ldg(c.ks + blk), vs = __ldg(c.vs + blk);
-        } else {
-          ks = 1.f, vs = -1.f;
         }
+        if (j < J) load(w, j, at, is_full(j, at));
       };
-      scales_at(at);
-      load(0, at, is_full(0, at));
-      for (int j = 0; j < J; ++j, ++block) {
-        const uint32_t s = block & 1u;
-        const float ks_now = ks, vs_now = vs;
-        const int after = entry(j + 2);
-        at = from(next, j + 1);
-        scales_at(at);
-        next = after;
-        const bool whole = is_full(j + 1, at);
-        ok = tc::wait_warp(&empty[s], ((block >> 1) & 1u) ^ 1u, wd);
-        if (!ok) break;
+      auto convert = [&](uint4 (&w)[N], float& ks, float& vs, int j) {
+        const uint32_t s = block % STAGES;
+        if (!(ok = tc::wait_warp(&empty[s], ((block / STAGES) & 1u) ^ 1u, wd))) return;
         if (warp == 8) {
-          const float v = fmaxf(vs_now, 1e-30f);
-          if (lane < 8)
-            sm.scale[block & 3][lane] =
-                make_float4(fmaxf(ks_now, 1e-30f), vs_now < 0.f ? -CUDART_INF_F : __log2f(v),
-                            vs_now < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
+          const float v = fmaxf(vs, 1e-30f);
+          if (lane < TK / 16)
+            sm.scale[block % SCALES][lane] =
+                make_float4(fmaxf(ks, 1e-30f), vs < 0.f ? -CUDART_INF_F : __log2f(v),
+                            vs < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.scfull[block & 3]);
+          if (lane == 0) tc::mbar_arrive(&sm.scfull[block % SCALES]);
         }
-        store(region + s * S::TILE);
-        // (before the next loads: a release waits for loads on their way)
+        store(w, region + s * S::BLOCK);
         if (lane == 0) tc::mbar_arrive(&full[s]);
-        if (j + 1 < J) load(j + 1, at, whole);
+        ++block;
+        fetch(w, ks, vs, j + 2);
+      };
+      fetch(w0, ks0, vs0, 0);
+      fetch(w1, ks1, vs1, 1);
+      for (int j = 0; j < J && ok; j += 2) {
+        convert(w0, ks0, vs0, j);
+        if (j + 1 < J && ok) convert(w1, ks1, vs1, j + 1);
       }
     }
     if (!ok) sm.abort_flag = 1;
@@ -634,63 +648,65 @@ __global__ void __launch_bounds__(THREADS, 1)
     // (the whole warp walks the loop and one lane issues, so that operand
     // addresses stay in uniform registers)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
-    constexpr uint32_t idesc_s = idesc_f16(128, false), idesc_o = idesc_f16(D, true);
-    uint32_t block = 0, seg = 0, opx0 = 0, opx1 = 0;
-    bool ok = warp == 16;
+    constexpr uint32_t idesc_s = idesc_f16(TK, false), idesc_o = idesc_f16(D, true);
+    // Each tile has a warp of its own.  A tile's rounds so far: scores issued,
+    // weights taken.
+    const int x = warp & 1;
+    uint32_t block = 0, seg = 0, sc = 0, pv = 0;
+    bool ok = warp < 18;
     for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
-      const int J = wk.t1 - wk.t0, N = PAIR ? 2 * J : J;
+      const int J = wk.t1 - wk.t0, N = PAIR ? J : (J + 1 - x) >> 1;
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
       tc::fence_after_sync();
-      // scores of round k: tile k & 1, block k / 2 (PAIR) or k
-      auto scores = [&](int k) {
-        const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
-        if (!tc::wait_warp(&sm.kfull[s], (b >> 1) & 1u, wd)) return false;
+      const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
+      auto scores = [&](int i) {
+        const uint32_t b = block + (PAIR ? i : 2 * i + x), s = b % STAGES, buf = sc & 1u;
+        if (!tc::wait_warp(&sm.kfull[s], (b / STAGES) & 1u, wd)) return false;
         tc::fence_after_sync();
-        const uint64_t dk = tc::sdesc_k_sw128(ksm + s * S::TILE);
-        const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
+        ++sc;
+        const uint64_t dk = tc::sdesc_k_sw128(ksm + s * S::BLOCK);
         if (tc::elect_one()) {
 #pragma unroll
           for (int term = 0; term < (TWO ? 2 : 1); ++term)
 #pragma unroll
             for (int k16 = 0; k16 < D / 16; ++k16) {
-              const uint32_t at = ((k16 / 4) * PLANE + (k16 & 3) * 32) >> 4;
-              tc::mma_f16_ss(tmem + x * 128, dq + uint64_t(term * (S::TILE >> 4) + at),
-                             dk + uint64_t(at), idesc_s, (term | k16) != 0);
+              const uint32_t qat = ((k16 / 4) * PLANE + (k16 & 3) * 32) >> 4;
+              const uint32_t kat = ((k16 / 4) * KVPLANE + (k16 & 3) * 32) >> 4;
+              tc::mma_f16_ss(tmem + x * 128 + buf * TK, dq + uint64_t(term * (S::TILE >> 4) + qat),
+                             dk + uint64_t(kat), idesc_s, (term | k16) != 0);
             }
-          tc::mma_commit(&sm.sfull[x]);
-          if (!PAIR || x == 1) tc::mma_commit(&sm.kempty[s]);
+          tc::mma_commit(&sm.sfull[x][buf]);
+          tc::mma_commit(&sm.kempty[s]);
         }
         __syncwarp();
         return true;
       };
-      for (int k = 0; k < 2 && k < N && ok; ++k) ok = scores(k);
-      for (int k = 0; k < N && ok; ++k) {
-        const uint32_t b = block + (PAIR ? k >> 1 : k), s = b & 1u, x = k & 1;
-        if (!(ok = tc::wait_warp(&sm.vfull[s], (b >> 1) & 1u, wd))) break;
-        if (!(ok = tc::wait_warp(&sm.pfull[x], (x ? opx1 : opx0) & 1u, wd))) break;
-        if (x)
-          ++opx1;
-        else
-          ++opx0;
+      // the scores are two rounds ahead of their weights
+      for (int i = 0; i < 2 && i < N && ok; ++i) ok = scores(i);
+      for (int i = 0; i < N && ok; ++i) {
+        const uint32_t b = block + (PAIR ? i : 2 * i + x), s = b % STAGES, buf = pv & 1u;
+        if (!(ok = tc::wait_warp(&sm.vfull[s], (b / STAGES) & 1u, wd))) break;
+        if (!(ok = tc::wait_warp(&sm.pfull[x][buf], (pv >> 1) & 1u, wd))) break;
+        ++pv;
         tc::fence_after_sync();
-        const uint64_t dv = sdesc_mn_sw128(vsm + s * S::TILE, PLANE);
+        const uint64_t dv = sdesc_mn_sw128(vsm + s * S::BLOCK, KVPLANE);
         if (tc::elect_one()) {
 #pragma unroll
           for (int k16 = 0; k16 < TK / 16; ++k16)
-            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + k16 * 8, dv + uint64_t(k16 * 128),
-                           idesc_o, k > 1 || k16 != 0);
-          tc::mma_commit(&sm.odone[x]);
-          if (!PAIR || x == 1) tc::mma_commit(&sm.vempty[s]);
+            tc::mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + buf * TK + k16 * 8,
+                           dv + uint64_t(k16 * 128), idesc_o, i > 0 || k16 != 0);
+          tc::mma_commit(&sm.odone[x][buf]);
+          tc::mma_commit(&sm.vempty[s]);
         }
         __syncwarp();
-        if (k + 2 < N) ok = scores(k + 2);
+        if (i + 2 < N) ok = scores(i + 2);
       }
       block += J;
     }
-    if (!ok && warp == 16) sm.abort_flag = 1;
-    if (warp == 16 && tc::elect_one()) {
-      tc::mma_commit(&sm.drain);
-      tc::wait_until(&sm.drain, 0, tc::globaltimer_ns() + tc::kDrainNs);
+    if (!ok && warp < 18) sm.abort_flag = 1;
+    if (warp < 18 && tc::elect_one()) {
+      tc::mma_commit(&sm.drain[x]);
+      tc::wait_until(&sm.drain[x], 0, tc::globaltimer_ns() + tc::kDrainNs);
     }
     __syncwarp();
   }
