@@ -48,6 +48,65 @@ constexpr int STAGES = 4;   // blocks of keys and of values in shared memory
 constexpr int SCALES = 8;   // blocks whose scales are kept
 constexpr int START = 4;    // units an item's queries and results count
 
+// An item's (sequence, row tile) and how many blocks it has.
+struct Item {
+  int b, r, h;
+  int n, q0, len, R, tiles;
+  __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int rows, int* status) {
+    n = seq_rows(bt, b, &q0, status);
+    len = __ldg(bt.lens + b);
+    const int64_t most = int64_t(bt.width) << tshift;
+    if (len < 0 || len > most) {
+      record_error(status, WQ_ERR_ARG);
+      len = len < 0 ? 0 : int(most);
+    }
+    R = int((int64_t(n) * G + rows - 1) / rows);
+    row_tile(G, rows);
+  }
+  __device__ __forceinline__ void row_tile(int G, int rows) {
+    int64_t i = (int64_t(r + 1) * rows - 1) / G;  // the tile's last query
+    if (i > n - 1) i = n - 1;
+    int seen = len - n + int(i) + 1;
+    seen = seen > len ? len : seen;
+    tiles = seen > 0 ? (seen + TK - 1) / TK : 1;
+  }
+  __device__ __forceinline__ bool valid() const { return n > 0 && r < R; }
+};
+
+// Walks over the work of a CTA's run: the item and its blocks [t0, t1).
+struct Walk {
+  Item it;
+  int64_t begin, u0, u1;  // first unit of the item; the run
+  int t0, t1;
+  bool first;
+  __device__ __forceinline__ void clip() {
+    const int64_t a = u0 - begin - START, e = u1 - begin - START;
+    t0 = a > 0 ? int(a) : 0;
+    t1 = e < it.tiles ? int(e) : it.tiles;
+  }
+  // the next item with blocks in the run; false at its end
+  __device__ __forceinline__ bool next(const Batch& bt, int heads, int tshift, int G, int rows) {
+    while (true) {
+      begin += it.tiles + START;
+      if (begin >= u1) return false;
+      if (++it.h == heads) {
+        it.h = 0;
+        if (++it.r < it.R) {
+          it.row_tile(G, rows);
+        } else {
+          it.r = 0;
+          do {
+            if (++it.b >= bt.B) return false;
+            it.load(bt, tshift, G, rows, nullptr);
+          } while (it.n == 0);
+        }
+      }
+      clip();
+      if (t1 > t0) return true;
+    }
+  }
+};
+
 template <int D>
 struct Smem {
   static constexpr int TILE = 128 * D * 2;  // 128 rows of f16
@@ -65,6 +124,9 @@ struct Smem {
     float4 scale[SCALES][TK / 16];
     float m[128], l[128];   // of tile 1, where both tiles are the same rows
     int64_t sum[WARPS], start_off;
+    // every warp's place in the work (in registers it would be spilled, and local
+    // memory comes back from L2 here)
+    Walk walk[WARPS];
     int start_p, tmem_base, abort_flag;
   };
   static constexpr size_t BYTES = 1024 + BLOCKS + sizeof(Ctrl);
@@ -123,65 +185,6 @@ struct TcArgs {
   float* parts;     // [2 W][ROWS][D]
   float* part_ml;   // [2 W][ROWS][2]
   Cut* cuts;        // [W] the items that the runs' starts cut
-};
-
-// An item's (sequence, row tile) and how many blocks it has.
-struct Item {
-  int b, r, h;
-  int n, q0, len, R, tiles;
-  __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int rows, int* status) {
-    n = seq_rows(bt, b, &q0, status);
-    len = __ldg(bt.lens + b);
-    const int64_t most = int64_t(bt.width) << tshift;
-    if (len < 0 || len > most) {
-      record_error(status, WQ_ERR_ARG);
-      len = len < 0 ? 0 : int(most);
-    }
-    R = int((int64_t(n) * G + rows - 1) / rows);
-    row_tile(G, rows);
-  }
-  __device__ __forceinline__ void row_tile(int G, int rows) {
-    int64_t i = (int64_t(r + 1) * rows - 1) / G;  // the tile's last query
-    if (i > n - 1) i = n - 1;
-    int seen = len - n + int(i) + 1;
-    seen = seen > len ? len : seen;
-    tiles = seen > 0 ? (seen + TK - 1) / TK : 1;
-  }
-  __device__ __forceinline__ bool valid() const { return n > 0 && r < R; }
-};
-
-// Walks over the work of a CTA's run: the item and its blocks [t0, t1).
-struct Walk {
-  Item it;
-  int64_t begin, u0, u1;  // first unit of the item; the run
-  int t0, t1;
-  bool first;
-  __device__ __forceinline__ void clip() {
-    const int64_t a = u0 - begin - START, e = u1 - begin - START;
-    t0 = a > 0 ? int(a) : 0;
-    t1 = e < it.tiles ? int(e) : it.tiles;
-  }
-  // the next item with blocks in the run; false at its end
-  __device__ __forceinline__ bool next(const Batch& bt, int heads, int tshift, int G, int rows) {
-    while (true) {
-      begin += it.tiles + START;
-      if (begin >= u1) return false;
-      if (++it.h == heads) {
-        it.h = 0;
-        if (++it.r < it.R) {
-          it.row_tile(G, rows);
-        } else {
-          it.r = 0;
-          do {
-            if (++it.b >= bt.B) return false;
-            it.load(bt, tshift, G, rows, nullptr);
-          } while (it.n == 0);
-        }
-      }
-      clip();
-      if (t1 > t0) return true;
-    }
-  }
 };
 
 template <typename TQ, int FMT, int D, bool PAIR>
@@ -282,6 +285,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = uint32_t(sm.tmem_base);
   const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
   bool more = wk.t1 > wk.t0 || wk.next(bt, c.heads, c.tshift, ar.G, ROWS);
+  if (lane == 0) sm.walk[warp] = wk;
+  __syncwarp();
+  const Walk& place = sm.walk[warp];
+  const Item& it = place.it;
+  auto step = [&]() {
+    Walk w = place;
+    const bool m = w.next(bt, c.heads, c.tshift, ar.G, ROWS);
+    __syncwarp();
+    if (lane == 0) sm.walk[warp] = w;
+    __syncwarp();
+    return m;
+  };
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
@@ -295,8 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t op = 0;  // tensor-core rounds of this tile so far
     bool ok = true, first_seg = true;
     uint32_t block = 0, seg = 0;  // blocks and items of the CTA so far
-    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
-      const Item& it = wk.it;
+    for (; more && ok; more = step(), ++seg) {
       const int rr = it.r * ROWS + (PAIR ? x * 128 : 0) + row;
       const bool live = rr < it.n * ar.G;
       const int i = live ? rr / ar.G : 0;
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
 
       float m = -CUDART_INF_F, l = 0.f;
-      const int J = wk.t1 - wk.t0;
+      const int t0 = place.t0, J = place.t1 - t0;
       int done = 0;  // of this tile in this segment
       for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
         const uint32_t b = block + uint32_t(j);
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                    tc::wait_warp(&sm.scfull[b % SCALES], (b / SCALES) & 1u, wd)))
           break;
         tc::fence_after_sync();
-        const int tok0 = (wk.t0 + j) * TK;
+        const int tok0 = (t0 + j) * TK;
         const float4* scl = sm.scale[b % SCALES];
         // -------- weights against the maximum so far; where a score is more than
         // LAG above it the maximum moves and they are computed again
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_after_sync();
       }
       // -------- results
-      const bool whole = wk.t0 == 0 && wk.t1 == it.tiles;
+      const bool whole = place.t0 == 0 && place.t1 == it.tiles;
       const int64_t part = int64_t(blockIdx.x) * 2 + (first_seg ? 0 : 1);
       float w0 = 1.f, w1 = 0.f;
       bool both = false;
@@ -541,15 +555,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int plane = piece / 4, part0 = (piece & 3) * 2, swap = plane & 1;
     uint32_t block = 0;
     bool ok = true;
-    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS)) {
-      const Item& it = wk.it;
-      const int J = wk.t1 - wk.t0;
+    for (; more && ok; more = step()) {
+      const int t0 = place.t0, J = place.t1 - t0, len = it.len;
       // Lane g of a warp looks after positions 16 g to 16 g + 15 of a block (one
       // page): table entry two blocks ahead, address and (first warp) scales one
       // block ahead, so that nothing here waits for the load before it.
       auto entry = [&](int j) {
-        const int tok = (wk.t0 + j) * TK + lane * 16;
-        return lane < TK / 16 && j < J && tok < it.len
+        const int tok = (t0 + j) * TK + lane * 16;
+        return lane < TK / 16 && j < J && tok < len
                    ? __ldg(bt.table + int64_t(it.b) * bt.width + (tok >> c.tshift))
                    : -2;
       };
@@ -558,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (page != -2) record_error(status, WQ_ERR_ARG);
           return int64_t(-1);
         }
-        return ((c.block(page, it.h) << c.tshift) + (((wk.t0 + j) * TK + lane * 16) & (T_ - 1))) * D;
+        return ((c.block(page, it.h) << c.tshift) + (((t0 + j) * TK + lane * 16) & (T_ - 1))) * D;
       };
       auto load = [&](uint4 (&w)[N], int j, int64_t at, bool whole) {
         const uint8_t* mine = src + (tr & 15) * D + piece * 16;
@@ -574,13 +587,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = tr + i * STEP;
             const int64_t o = __shfl_sync(0xffffffffu, at, r >> 4);
             w[i] = make_uint4(0, 0, 0, 0);
-            if (o >= 0 && (wk.t0 + j) * TK + r < it.len)
+            if (o >= 0 && (t0 + j) * TK + r < len)
               w[i] = __ldg(reinterpret_cast<const uint4*>(mine + o));
           }
         }
       };
       auto is_full = [&](int j, int64_t at) {
-        return (wk.t0 + j + 1) * TK <= it.len && __all_sync(0xffffffffu, lane >= TK / 16 || at >= 0);
+        return (t0 + j + 1) * TK <= len && __all_sync(0xffffffffu, lane >= TK / 16 || at >= 0);
       };
       auto store = [&](const uint4 (&w)[N], uint32_t dst) {
 #pragma unroll
@@ -654,8 +667,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int x = warp & 1;
     uint32_t block = 0, seg = 0, sc = 0, pv = 0;
     bool ok = warp < 18;
-    for (; more && ok; more = wk.next(bt, c.heads, c.tshift, ar.G, ROWS), ++seg) {
-      const int J = wk.t1 - wk.t0, N = PAIR ? J : (J + 1 - x) >> 1;
+    for (; more && ok; more = step(), ++seg) {
+      const int J = place.t1 - place.t0, N = PAIR ? J : (J + 1 - x) >> 1;
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
       tc::fence_after_sync();
       const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
