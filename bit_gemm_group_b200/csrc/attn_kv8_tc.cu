@@ -843,7 +843,7 @@ int launch_tc_by_type(const void* Q, int dtype, int64_t ldq, int64_t heads, cons
 // Whether the tensor-memory kernel takes the call: more than 8 rows to a
 // (sequence, kv head), heads of 64 or 128.
 bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
-  return D <= 128 && max_q * (heads / kv_heads) > 8;
+  return D <= 128 && max_q * (heads / kv_heads) > 64;
 }
 bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
   return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
