@@ -415,11 +415,27 @@ def _addr(t):
     return t.data_ptr()
 
 
+# What every call asks of the CUDA context, without the objects and checks that
+# torch.cuda wraps around it (they cost a small call more than its kernel): the
+# handle of a device's current stream, and the current device.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_entry = {}
+
+
+def _entry_point(name):
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    return fn
+
+
 def _call(dev, name, stream, *args):
     """Call an entry point on device `dev` (the library works on the current one), on its
     current stream unless given."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
+    fn = _entry.get(name) or _entry_point(name)
+    if _current_device() == dev:
         st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
@@ -428,23 +444,16 @@ def _call(dev, name, stream, *args):
         raise WQError(st, name)
 
 
-# handle of the current stream of a device (torch.cuda.current_stream builds an object,
-# which costs a microsecond of every call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
 def _workspace(like, name, *sizes):
     """An uninitialised workspace on the device of `like`, of the size that `name` says."""
     dev = like.get_device()
     if dev < 0:
         raise WQError(WQ_ERR_ARG, "tensor is not on a CUDA device (no CPU fallback)")
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
-        n = fn(*sizes)
+    if _current_device() == dev:
+        n = _entry_point(name)(*sizes)
     else:
         with torch.cuda.device(dev):
-            n = fn(*sizes)
+            n = _entry_point(name)(*sizes)
     return like.new_empty((max(1, n),), dtype=torch.uint8)
 
 
