@@ -39,9 +39,9 @@ namespace kv8 {
 namespace tcore {
 
 // 20 warps of 96 registers at launch; the softmax keeps a block's 64 words of
-// weights and takes 136, the converters 80, the issuer's four warps 48
+// weights and takes 128, the converters 80, the issuers' four warps 64
 constexpr int WARPS = 20, THREADS = WARPS * 32;
-constexpr int REGS_SOFTMAX = 136, REGS_CONVERT = 80, REGS_ISSUE = 48;
+constexpr int REGS_SOFTMAX = 128, REGS_CONVERT = 80, REGS_ISSUE = 64;
 static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * 96, "registers");
 constexpr int TK = 64;      // positions per block
 constexpr int STAGES = 4;   // blocks of keys and of values in shared memory
@@ -164,6 +164,7 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t& a, uint32_t& b) {
   }
 }
 
+__device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
 __device__ __forceinline__ uint64_t u32x2(uint32_t a, uint32_t b) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
@@ -387,36 +388,43 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
           float mx = -CUDART_INF_F;
           sum = 0.f;
-          uint32_t s[2][16];
-          tc::tmem_ld_x16(st, s[0]);
+          uint32_t s[2][32];
+          tc::tmem_ld_x32(st, s[0]);
 #pragma unroll
-          for (int q = 0; q < TK / 16; ++q) {  // 16 positions, of one page
-            const float4 f = scl[q];
+          for (int c = 0; c < TK / 32; ++c) {
             tc::tmem_wait_ld();
-            if (q + 1 < TK / 16) tc::tmem_ld_x16(st + (q + 1) * 16, s[(q + 1) & 1]);
-            uint32_t(&v)[16] = s[q & 1];
+            if (c + 1 < TK / 32) tc::tmem_ld_x32(st + (c + 1) * 32, s[(c + 1) & 1]);
+            uint32_t(&v)[32] = s[c & 1];
             if (edge)
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (tok0 + q * 16 + e >= lim) v[e] = 0xFF800000u;
-            const float mul = fmaxf(fq * f.x, 1e-37f);
-            float a = __uint_as_float(v[0]);
+              for (int e = 0; e < 32; ++e)
+                if (tok0 + c * 32 + e >= lim) v[e] = 0xFF800000u;
 #pragma unroll
-            for (int e = 1; e < 16; ++e) a = fmaxf(a, __uint_as_float(v[e]));
-            mx = fmaxf(mx, fmaf(a, mul, f.y));
-            const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(f.y + off, f.y + off);
-            uint64_t part = 0;
+            for (int h = 0; h < 2; ++h) {  // 16 positions, of one page
+              const float4 f = scl[2 * c + h];
+              const float mul = fmaxf(fq * f.x, 1e-37f);
+              // (a tree of maxima of three)
+              float a[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint64_t t = u32x2(v[2 * e], v[2 * e + 1]);
-              asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(t) : "l"(mul2), "l"(add2));
-              const float x0 = exp2_approx(__uint_as_float(uint32_t(t)));
-              const float x1 = exp2_approx(__uint_as_float(uint32_t(t >> 32)));
-              const uint64_t y = f32x2(x0, x1);
-              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part) : "l"(y));
-              p[q * 8 + e] = f16x2(x0, x1);
+              for (int k = 0; k < 4; ++k)
+                a[k] = fmaxf(fmaxf(as_f(v[16 * h + 4 * k]), as_f(v[16 * h + 4 * k + 1])),
+                             fmaxf(as_f(v[16 * h + 4 * k + 2]), as_f(v[16 * h + 4 * k + 3])));
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), mul, f.y));
+              const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(f.y + off, f.y + off);
+              uint64_t part[2] = {0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                uint64_t t = u32x2(v[16 * h + 2 * e], v[16 * h + 2 * e + 1]);
+                asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(t) : "l"(mul2), "l"(add2));
+                const float x0 = exp2_approx(as_f(uint32_t(t)));
+                const float x1 = exp2_approx(as_f(uint32_t(t >> 32)));
+                const uint64_t y = f32x2(x0, x1);
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[e & 1]) : "l"(y));
+                p[c * 16 + h * 8 + e] = f16x2(x0, x1);
+              }
+              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[0]) : "l"(part[1]));
+              sum = fmaf(as_f(uint32_t(part[0])) + as_f(uint32_t(part[0] >> 32)), f.z, sum);
             }
-            sum = fmaf(__uint_as_float(uint32_t(part)) + __uint_as_float(uint32_t(part >> 32)), f.z, sum);
           }
           if (!__any_sync(0xffffffffu, mx > m + LAG)) break;
           const float now = fmaxf(m, mx);
@@ -440,11 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok) break;
         l += sum;
-#pragma unroll
-        for (int q = 0; q < TK / 32; ++q) {
-          uint32_t(&v)[16] = *reinterpret_cast<uint32_t(*)[16]>(&p[q * 16]);
-          tc::tmem_st_x16(st + q * 16, v);
-        }
+        tc::tmem_st_x32(st, p);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
