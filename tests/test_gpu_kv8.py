@@ -288,3 +288,85 @@ def test_captured_step_replayed_as_the_sequences_grow():
         assert bool(((out.cpu().double() - ref).abs() <= tol).all())
         assert torch.equal(y, wq.gemm_fp8_block(out.view(B, heads * D), q2, s2))
         lens = lens + 1
+
+
+@pytest.mark.parametrize("n", [1, 9])
+def test_many_sequences(n):
+    # more sequences than a CTA looks at in one go, most of them without rows; with 9 rows of 8
+    # heads each on the kernel for many rows
+    G = 8
+    seqs = [(n, 20 + b % 50) if b % 7 == 0 else (0, 5) for b in range(1500)]
+    seqs[-1] = (n, 40)
+    st = plain.make_state(seqs, G, 1, 64, 16, I8, BF, seed=11)
+    cache = plain.append(st["K"], st["V"], st["cache"], st["table"], st["cu"], st["lens"], None)
+    d = run_append(st)
+    check_cache(d, cache)
+    check_attention(st, d, cache)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_pages_beyond_32_bit_offsets(n):
+    # 4.5 GB of codes each for keys and values; the pages in use are the last ones
+    D, T, kv, G = 128, 128, 2, 4
+    st = plain.make_state([(n, 300), (n, 129)], kv * G, kv, D, T, E4, BF, seed=12)
+    used = st["cache"][0].shape[0]
+    pages = (9 << 29) // (kv * T * D)
+    assert (pages - used) * kv * T * D > 1 << 32
+    small = st["cache"]
+    big = tuple(torch.empty((pages,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in small)
+    for b, t in zip(big, small):
+        b[-used:] = t.cuda()
+    want = plain.append(st["K"], st["V"], small, st["table"], st["cu"], st["lens"], None)
+    d = plain.on_gpu(st)
+    d["cache"] = big
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - used), d["table"])
+    wq.kv8_append(d["K"], d["V"], big, d["table"], d["cu"], d["lens"], n, None)
+    for b, w in zip(big, want):
+        assert same_bytes(b[-used:].contiguous(), w)
+    check_attention(st, d, want)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_two_calls_at_once_on_streams_of_their_own(n):
+    states = [plain.make_state([(n, 700 + 90 * i), (n, 65)], 8, 2, 128, 64, I8, BF, seed=13 + i)
+              for i in range(2)]
+    wants, ds = [], []
+    for st in states:
+        wants.append(plain.append(st["K"], st["V"], st["cache"], st["table"], st["cu"], st["lens"],
+                                  None))
+        ds.append(plain.on_gpu(st))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                d = ds[i]
+                wq.kv8_append(d["K"], d["V"], d["cache"], d["table"], d["cu"], d["lens"], n)
+                outs[i].append(wq.attn_kv8(d["Q"], d["cache"], d["table"], d["cu"], d["lens"], n))
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_cache(ds[i], wants[i])
+        first = check_attention(states[i], ds[i], wants[i])
+        for o in outs[i]:
+            assert torch.equal(o, first)
+
+
+def test_sequences_that_share_a_prefix_read_the_same_pages():
+    # two sequences whose first pages are the same, each with a last page of its own
+    st = plain.make_state([(4, 196), (4, 196)], 4, 2, 64, 64, I8, BF, seed=15)
+    st["table"][1, :3] = st["table"][0, :3]
+    want = plain.append(st["K"], st["V"], st["cache"], st["table"], st["cu"], st["lens"], None)
+    d = run_append(st)
+    check_cache(d, want)
+    check_attention(st, d, want)
+
+
+def test_more_new_rows_than_positions_see_nothing_before_the_start():
+    # 6 rows of a sequence of 2 positions: the first four lie before its start
+    st = plain.make_state([(2, 2)], 4, 2, 64, 16, I8, BF, seed=16)
+    d = run_append(st)
+    Q = torch.randn(6, 4, 64, device="cuda", dtype=BF)
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    out = wq.attn_kv8(Q, d["cache"], d["table"], cu, d["lens"], 6)
+    assert bool((out[:4] == 0).all()) and bool((out[4:] != 0).any(-1).all())
