@@ -5,22 +5,30 @@
 //   s_j = scale (rope(q) . kq_j) ks(page of j),  j <= len - n + i
 //   o   = sum_j softmax(s)_j vq_j vs(page of j)
 //
-// Bound by HBM: every code is read once per block of 8 rows, 2 D bytes per
-// position and head.  The codes go to f16 (exactly: int8 and E4M3 are subsets)
-// and through mma.sync m16n8k16.  The scores' products have 16 rows for 8
-// queries: rows 0 to 7 hold the rotated query rounded to f16, rows 8 to 15 what
-// that rounding left, so that the query counts with 22 bits at no cost.  A
-// decode step needs about a third of the mma.sync rate while it streams at the
-// copy rate, so tensor memory would add hand-offs and no speed.
+// Bound by HBM up to 8 rows to a kv head: every code is read once per block of 8
+// rows, 2 D bytes per position and head.  64 sequences of 277580 positions in all,
+// 64 heads of 128 over 8 kv heads, one new token each (int8): 119 us with the
+// join, 4.8 TB/s.
+// Each further block of 8 rows reads the codes again (from L2, mostly) and expands
+// them again: 40 us per 4 x 32768 positions and 8 kv heads.
+//
+// The codes go to f16 (exactly: int8 and E4M3 are subsets) and through mma.sync
+// m16n8k16.  The scores' products have 16 rows for 8 queries: rows 0 to 7 hold the
+// rotated query rounded to f16, rows 8 to 15 what that rounding left, so that the
+// query counts with 22 bits at no cost.  A decode step needs about a third of the
+// mma.sync rate while it streams at the copy rate, so tensor memory would add
+// hand-offs and no speed.
 //
 // Work is cut into units of TK positions of one (sequence, head, row block),
-// numbered with the position fastest, and every warp of the grid takes an
-// equal run of them, whatever the sequences' lengths: no warp waits for
-// another.  A segment (all units of a row block) counts two units more, for its
-// queries and its result: a unit takes a warp 2.6 us in a full decode step, a
-// segment's start and end about 5, and without that the warps that got many
-// short sequences ended a quarter later than the rest.  A run's whole segments are written out directly; cut ones go to
-// the workspace and attn_kv8_join_kernel adds them in a fixed order.
+// numbered with the position fastest, and every warp of the grid takes an equal
+// run of them, whatever the sequences' lengths: no warp waits for another.  A
+// segment (all units of a row block) counts two units more, for its queries and
+// its result: a unit takes a warp 2.6 us in a full decode step, a segment's start
+// and end about 5, and without that the warps that got many short sequences ended
+// a quarter later than the rest.  A run's whole segments are written out directly;
+// cut ones go to the workspace and attn_kv8_join_kernel adds them in a fixed order
+// (10 us of those 119; its launch overlaps the end of the main kernel).
+// (Units of 16 positions for heads of 128: 147 us where these took 131.)
 //
 // Softmax in one pass, in base 2, with the value scale folded into the
 // exponent: t = s log2(e) + log2(vs), p' = 2^(t - m), so that p' is at most

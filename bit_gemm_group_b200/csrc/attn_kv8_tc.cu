@@ -1,16 +1,18 @@
-// attn_kv8_tc.cu -- causal attention over the paged 8-bit cache for more than 8
-// rows to a (sequence, kv head): prompts, chunks of prompts, drafts.
+// attn_kv8_tc.cu -- causal attention over the paged 8-bit cache for more than 32
+// rows to a (sequence, kv head): prompts, chunks of prompts, long drafts.
 //
 // The mathematics of attn_kv8.cu on the fifth-generation tensor cores.  One CTA
-// per SM; 128 rows (query, head) are one tensor-core tile:
+// per SM; 128 rows (query, head) are one tensor-core tile, 64 positions a block:
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a row per thread: scores
-//                   from tensor memory, weights back to it as f16
-//   warps 8-11      converters of keys: 128 positions of codes at a time from the
-//                   pages to f16 (exactly) in shared memory
+//                   from tensor memory, weights back to it as f16, over the scores
+//   warps 8-11      converters of keys: a block's codes from the pages to f16
+//                   (exactly) in shared memory, two blocks' loads ahead
 //   warps 12-15     converters of values, into the same 128-byte swizzled layout
 //                   (the product's sum runs along their rows: MN-major)
-//   warps 16, 17    issue, a warp per tile, tcgen05.mma kind::f16: scores Q K^T (both operands
-//                   in shared memory), then weights (tensor memory) times V
+//   warps 16, 17    issue, a warp per tile, tcgen05.mma kind::f16: scores Q K^T
+//                   (both operands in shared memory), then weights (tensor
+//                   memory) times V; the scores run two blocks ahead
+//   warps 18, 19    no work (registers are given in groups of four warps)
 //
 // PAIR: the two tiles are 256 rows of one (sequence, head) and share every
 // converted block, which halves the conversion work: prompts.  Otherwise both
@@ -19,13 +21,20 @@
 // tensor cores work for the other), and fp16 inputs, whose queries are two f16
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
-// Bound by the tensor cores and the exponentials together: a 128 x 128 block of
-// scores is 2 x 512 cycles of MMA and 1024 of the special-function units at
-// D = 128.  With few rows it is bound by the blocks' latency.
+// Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
+// all (E4M3): 431 us, 546 TFLOP/s of products.  Bound by the hand-offs: a
+// block takes a tile 2600 cycles on average, of which its two products are 560
+// (64 cycles per m128 n64 k16 score step and 35 per m128 n128 k16 value step of
+// each tile) and its exponentials 512 of the special-function units.  Leaving one
+// part out at a time says that none of them is the limit by itself: no
+// exponentials 399 us, no converter stores 419, no converter loads either 409, no
+// sums 416; part of the exponentials as polynomials on the fma pipe 430 at best.
+// Two score buffers of 64 positions per tile let the tensor cores run while the
+// softmax works on the other.
 //
-// Items (row tile, head) are cut into blocks of 128 positions and numbered; each
-// CTA takes an equal run of blocks, with START more for each item, and joins
-// cut items as attn_kv8.cu does.
+// Items (row tile, head) are cut into blocks and numbered; each CTA takes an equal
+// run of blocks, with START more for each item, and joins cut items as attn_kv8.cu
+// does.
 #include <math_constants.h>
 
 #include <mutex>
@@ -78,7 +87,6 @@ struct Walk {
   Item it;
   int64_t begin, u0, u1;  // first unit of the item; the run
   int t0, t1;
-  bool first;
   __device__ __forceinline__ void clip() {
     const int64_t a = u0 - begin - START, e = u1 - begin - START;
     t0 = a > 0 ? int(a) : 0;
@@ -284,7 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = uint32_t(sm.tmem_base);
-  const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
+  // (the limit starts again with every item: a call may take longer than one wait)
+  tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
   bool more = wk.t1 > wk.t0 || wk.next(bt, c.heads, c.tshift, ar.G, ROWS);
   if (lane == 0) sm.walk[warp] = wk;
   __syncwarp();
@@ -296,6 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     if (lane == 0) sm.walk[warp] = w;
     __syncwarp();
+    wd.deadline_ns = tc::globaltimer_ns() + limit_ns;
     return m;
   };
 
@@ -844,11 +854,18 @@ int launch_tc_by_type(const void* Q, int dtype, int64_t ldq, int64_t heads, cons
 
 }  // namespace
 
-// Whether the tensor-memory kernel takes the call: more than 8 rows to a
-// (sequence, kv head), heads of 64 or 128.
+// Whether the tensor-memory kernel takes the call: more than 32 rows to a
+// (sequence, kv head).  The other kernel reads the codes once for each 8 rows, this
+// one once for 128 (its time hardly depends on the rows).  Measured, the other and
+// this, over 4 x 32768 positions of 8 kv heads of 128: 16 rows 116 and 182 us, 24
+// 165 and 182, 32 199 and 182, 40 235 and 184, 64 363 and 186; over 64 x 2048 32
+// rows 207 and 207; heads of 64, 32 rows 135 and 145, 40 165 and 147.  Results of
+// 256 elements for two tiles do not fit in tensor memory beside the scores.
 bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
-  return D <= 128 && max_q * (heads / kv_heads) > 64;
+  return D <= 128 && max_q * (heads / kv_heads) > 32;
 }
+// Two row tiles that share the converted blocks: where there are two (160 rows over
+// 4 x 32768: 223 us, and 336 one tile after the other), and the queries are one term.
 bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
   return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
 }

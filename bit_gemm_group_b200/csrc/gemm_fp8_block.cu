@@ -15,7 +15,9 @@
 //   gemm_fp8_block_split_kernel  (HBM or L2) 128 channels x NT tokens per
 //     tile, channels on the lanes: every SM streams the same number of
 //     (tile, K block) units whatever the shape; a tile cut between CTAs is
-//     joined, in K order, by the CTA that arrives last.
+//     joined, in K order, by the CTA that arrives last.  1 x 28672 x 8192: 51
+//     us, 4.6 TB/s with the quantizer's launch and the join (about 11 us that do
+//     not depend on the weights: at 16 x 4096 x 11008 they are half of 19 us).
 #include <mutex>
 
 #include "kernels.h"
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  const tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
+  // (the limit starts again with every tile: a product may take longer than one wait)
+  tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
   // the quantizer's codes and scales of X are complete from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        wd.deadline_ns = tc::globaltimer_ns() + limit_ns;
         const int mt = tile % mtiles, nt = tile / mtiles;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
@@ -151,6 +155,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        wd.deadline_ns = tc::globaltimer_ns() + limit_ns;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
           const uint32_t buf = it & 1u;
@@ -184,6 +189,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      wd.deadline_ns = tc::globaltimer_ns() + limit_ns;
       const int mt = tile % mtiles, nt = tile / mtiles;
       const int row0 = mt * BM + q * 32;
       const int n0 = nt * BN + part * 64;
@@ -519,10 +525,21 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Tokens per tile of the split kernel, or 0 for the large-product kernel.
-int split_tokens(int64_t M, int64_t N) {
-  const int64_t large = ((M + 127) / 128) * ((N + 255) / 256);
-  if (M > 128 && large >= 96) return 0;
+// Tokens per tile of the split kernel, or 0 for the large-product kernel.  A K
+// block takes a CTA of the large kernel 0.43 us for 128 x 256 sums, one of the
+// split kernel 0.5 us for 128 x 128 (a quarter less for 128 x 64), but those are
+// shared out evenly over the SMs and their join takes about as long as 30 (22).
+// Measured, large and split, with weights from HBM: 96 x 2048 x 4096 24.6 and
+// 30.7 us, 96 x 2048 x 8192 38.9 and 32.8, 129 x 8192 x 8192 45 and 51, 129 x
+// 4096 x 8192 41 and 37, 96 x 28672 x 11008 76 and 92, 384 x 16384 x 4096 47 and
+// 72, 64 x 28672 x 4096 37 and 45, 64 x 8192 x 8192 41 and 33; within a tenth
+// near the border.  Up to 32 tokens the split kernel is as fast or faster but for
+// K near 2048 (17 x 28672 x 2048: 24.6 and 28.7).
+int split_tokens(int64_t M, int64_t N, int64_t K) {
+  const int64_t kb = (K + 127) / 128, mt = (M + 127) / 128, sms = sm_count();
+  const int64_t waves = (mt * ((N + 255) / 256) + sms - 1) / sms;
+  const int64_t units = mt * ((N + 127) / 128) * kb / sms;
+  if (M > 32 && waves * kb <= (M > 64 ? units + 30 : units * 3 / 4 + 22)) return 0;
   return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
 }
 
@@ -536,7 +553,7 @@ struct Plan {
 Plan plan(int64_t M, int64_t N, int64_t K) {
   Plan p;
   const int64_t kb = (K + 127) / 128;
-  p.nt = split_tokens(M, N);
+  p.nt = split_tokens(M, N, K);
   p.mp = (M + 127) / 128 * 128;
   p.sx = up256(size_t(M) * size_t(K));
   p.counters = p.sx + up256(size_t(kb * p.mp) * 4);

@@ -15,6 +15,11 @@
 // that nothing is read twice; the loads of its four pieces are in flight
 // together.  In a decode step a CTA has one row; older codes are read only when
 // the new row raises the maximum.
+//
+// 7107 rows of 8 heads of 128 in four sequences: 23 us (the 44 MB at the copy
+// rate are 6.7; an unrotated, unquantized copy is not what bounds it but a CTA's
+// chain of table, rows, maximum, codes).  64 sequences with one row each: 9 to 12
+// us, the same chain once.
 #include "kv8.cuh"
 
 namespace wq {
