@@ -120,25 +120,33 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   const uint32_t tmem = sm.tmem_base;
   // (the limit starts again with every tile: a product may take longer than one wait)
   tc::Watchdog wd{tc::globaltimer_ns() + limit_ns, &sm.abort_flag, status};
-  // the quantizer's codes and scales of X are complete from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ISSUE));
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- producer
-      uint32_t it = 0;
+      // W does not depend on the quantizer of X, whose codes and scales are
+      // complete after griddepcontrol.wait: the first weight tiles come before it
+      uint32_t it = 0, pre = 0;
+      for (int tile = blockIdx.x; tile < total && pre < uint32_t(STAGES); tile += gridDim.x)
+        for (int kb = 0; kb < kblocks && pre < uint32_t(STAGES); ++kb, ++pre) {
+          tc::mbar_arrive_expect_tx(&sm.full[pre], STAGE_BYTES);
+          tc::tma_load_2d(tiles + size_t(pre) * STAGE_BYTES + A_BYTES, &tmB, &sm.full[pre], kb * BK,
+                          tile / mtiles * BN);
+        }
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       bool ok = true;
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         wd.deadline_ns = tc::globaltimer_ns() + limit_ns;
         const int mt = tile % mtiles, nt = tile / mtiles;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
-          if (!(ok = tc::wait_bounded(&sm.empty[s], ((it / STAGES) & 1u) ^ 1u, wd))) break;
           uint8_t* a = tiles + size_t(s) * STAGE_BYTES;
-          tc::mbar_arrive_expect_tx(&sm.full[s], STAGE_BYTES);
+          if (it >= pre) {
+            if (!(ok = tc::wait_bounded(&sm.empty[s], ((it / STAGES) & 1u) ^ 1u, wd))) break;
+            tc::mbar_arrive_expect_tx(&sm.full[s], STAGE_BYTES);
+            tc::tma_load_2d(a + A_BYTES, &tmB, &sm.full[s], kb * BK, nt * BN);
+          }
           tc::tma_load_2d(a, &tmA, &sm.full[s], kb * BK, mt * BM);
-          tc::tma_load_2d(a + A_BYTES, &tmB, &sm.full[s], kb * BK, nt * BN);
         }
       }
       // the last load issued into each stage has landed before exit
@@ -183,6 +191,7 @@ __global__ void __launch_bounds__(THREADS_L, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ADD));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int q = warp & 3;            // tensor-memory lane quarter
     const int part = (warp - 4) >> 2;  // channels [64 part, 64 part + 64) of the tile
     const uint32_t out = tc::smem_u32(outs + (warp - 4) * OUT_BYTES);

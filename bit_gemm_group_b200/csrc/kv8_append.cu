@@ -16,10 +16,12 @@
 // together.  In a decode step a CTA has one row; older codes are read only when
 // the new row raises the maximum.
 //
-// 7107 rows of 8 heads of 128 in four sequences: 23 us (the 44 MB at the copy
-// rate are 6.7; an unrotated, unquantized copy is not what bounds it but a CTA's
-// chain of table, rows, maximum, codes).  64 sequences with one row each: 9 to 12
-// us, the same chain once.
+// 7107 rows of 8 heads of 128 in four sequences: 18 us (their 44 MB at the copy
+// rate are 6.7), bound by a CTA's chain of table, rows, maximum and codes, about 5
+// us four times over, and by instructions: the quotients in packed pairs and one
+// test for all of a thread's non-finite elements took it from 23.  Half as many
+// elements in twice the threads: 16 us, but a step of 64 sequences with one row
+// each 9.2 us in place of 8.2.
 #include "kv8.cuh"
 
 namespace wq {
@@ -27,6 +29,8 @@ namespace kv8 {
 
 constexpr int STEPS = 4;  // 16-element pieces per thread; T D / 64 threads
 
+// (a, b) -> (a c - b s, b c + a s), every product and sum rounded (the packed
+// multiplication and addition come out fused: one bit off)
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
   b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
@@ -78,11 +82,8 @@ __global__ void __launch_bounds__(512)
   uint8_t* codes = (is_v ? c.vq : c.kq) + (blk << c.tshift) * D;
   float* sp = (is_v ? c.vs : c.ks) + blk;
 
-  // the new rows (beyond the last, that one again), NaN as 0; infinities keep
-  // their sign and saturate
-  float x[STEPS][16];
-  float m = 0.f;
-  bool bad = false;
+  // the new rows (beyond the last, that one again), in pairs of elements
+  uint64_t x[STEPS][8];
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const T* row = src + int64_t(min(first + i * rstep, rows - 1)) * ld;
@@ -92,7 +93,10 @@ __global__ void __launch_bounds__(512)
       load8(row + d1, b8);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = a[e], x[i][8 + e] = b8[e];
+    for (int e = 0; e < 4; ++e) {
+      x[i][e] = two(a[2 * e], a[2 * e + 1]);
+      x[i][4 + e] = two(b8[2 * e], b8[2 * e + 1]);
+    }
   }
   if (turns) {
 #pragma unroll
@@ -103,27 +107,59 @@ __global__ void __launch_bounds__(512)
       load8(rp.cos + at, cs);
       load8(rp.sin + at, sn);
       // pair e: elements e and e + 8 of the piece, or 2 e and 2 e + 1
-      if (split) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn(x[i][e], x[i][8 + e], cs[e], sn[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) turn(x[i][2 * e], x[i][2 * e + 1], cs[e], sn[e]);
+      for (int e = 0; e < 4; ++e) {
+        float a[2], b[2];
+        if (split) {
+          split_two(x[i][e], a[0], a[1]);
+          split_two(x[i][4 + e], b[0], b[1]);
+        } else {
+          split_two(x[i][2 * e], a[0], b[0]);
+          split_two(x[i][2 * e + 1], a[1], b[1]);
+        }
+        turn(a[0], b[0], cs[2 * e], sn[2 * e]);
+        turn(a[1], b[1], cs[2 * e + 1], sn[2 * e + 1]);
+        if (split) {
+          x[i][e] = two(a[0], a[1]);
+          x[i][4 + e] = two(b[0], b[1]);
+        } else {
+          x[i][2 * e] = two(a[0], b[0]);
+          x[i][2 * e + 1] = two(a[1], b[1]);
+        }
       }
     }
   }
+  // the largest magnitude; x 0 summed is no number where an element is not finite
+  float m = 0.f;
+  uint64_t odd = 0;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float a = fabsf(x[i][e]);
-      if (a <= 3.4028234663852886e38f) {
-        m = fmaxf(m, a);
-      } else {
-        bad = true;
-        if (a != a) x[i][e] = 0.f;
-      }
+    for (int e = 0; e < 8; ++e) {
+      float a, b;
+      split_two(x[i][e], a, b);
+      m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+      odd = fma_two(x[i][e], 0, odd);
     }
+  float odd0, odd1;
+  split_two(odd, odd0, odd1);
+  const bool bad = odd0 != 0.f || odd1 != 0.f;
+  if (bad) {  // of the finite ones; NaN as 0, infinities keep their sign and saturate
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v[2];
+        split_two(x[i][e], v[0], v[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (fabsf(v[k]) <= 3.4028234663852886e38f) m = fmaxf(m, fabsf(v[k]));
+          if (v[k] != v[k]) v[k] = 0.f;
+        }
+        x[i][e] = two(v[0], v[1]);
+      }
+  }
   const float old = slot0 ? *sp : 0.f;
   m = warp_max(m);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -154,7 +190,20 @@ __global__ void __launch_bounds__(512)
       *reinterpret_cast<uint32_t*>(codes + i) = o;
     }
   }
-  const float inv = __frcp_rn(s), top = s * TOP;
+  if (bad) {
+    const float top = s * TOP;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float a, b;
+        split_two(x[i][e], a, b);
+        x[i][e] = two(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+      }
+  }
+  // (a finite element is within half a unit of s TOP's last place, whose code is TOP)
+  const float inv = __frcp_rn(s);
+  const uint64_t minus = two(-s, -s), inv2 = two(inv, inv);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int r = first + i * rstep;
@@ -162,18 +211,23 @@ __global__ void __launch_bounds__(512)
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = quot_rn(fminf(fmaxf(x[i][4 * k + e], -top), top), s, inv);
+      uint64_t v[2] = {quot_rn_two(x[i][2 * k], minus, inv2),
+                       quot_rn_two(x[i][2 * k + 1], minus, inv2)};
+      float f[4];
       if (FMT == WQ_W8_INT8) {
         // the low byte of v + 1.5 2^23 is v rounded half to even
-        const float magic = 12582912.f;
-        o[k] = low_bytes4(__float_as_uint(v[0] + magic), __float_as_uint(v[1] + magic),
-                          __float_as_uint(v[2] + magic), __float_as_uint(v[3] + magic));
+        const uint64_t magic = two(12582912.f, 12582912.f);
+        v[0] = add_two(v[0], magic);
+        v[1] = add_two(v[1], magic);
+      }
+      split_two(v[0], f[0], f[1]);
+      split_two(v[1], f[2], f[3]);
+      if (FMT == WQ_W8_INT8) {
+        o[k] = low_bytes4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
       } else {
-        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
         o[k] = a | (b << 16);
       }
     }

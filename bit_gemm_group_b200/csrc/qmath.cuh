@@ -89,6 +89,38 @@ __device__ __forceinline__ float quot_rn(float x, float s, float y) {
   return fmaf(fmaf(-q, s, x), y, q);
 }
 
+// Two fp32 in one register pair, with the packed instructions on them (each half
+// rounded as by the plain instruction, at half the issue slots).
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_two(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// quot_rn of both halves; `minus` is -s twice, y fl(1 / s) twice.
+__device__ __forceinline__ uint64_t quot_rn_two(uint64_t x, uint64_t minus, uint64_t y) {
+  uint64_t q = mul_two(x, y);
+  q = fma_two(fma_two(q, minus, x), y, q);
+  return fma_two(fma_two(q, minus, x), y, q);
+}
+
 // The largest |x| (sym) or the smallest and largest x (asym) of a lane's 16
 // 16-bit elements, on the packed pairs.  NaN propagates (.NaN), so a lane
 // with a NaN or an infinity yields a non-finite statistic.
