@@ -22,13 +22,15 @@
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
 // Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
-// all (E4M3): 431 us, 546 TFLOP/s of products.  Bound by the hand-offs: a
-// block takes a tile 2600 cycles on average, of which its two products are 560
-// (64 cycles per m128 n64 k16 score step and 35 per m128 n128 k16 value step of
+// all (E4M3): 335 us, 702 TFLOP/s of products.  Bound by the hand-offs: a
+// block takes a tile 2600 cycles on average, of which its two products are 690
+// (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value step of
 // each tile) and its exponentials 512 of the special-function units.  Leaving one
-// part out at a time says that none of them is the limit by itself: no
+// part out at a time, at 431 us, says that none of them is the limit by itself: no
 // exponentials 399 us, no converter stores 419, no converter loads either 409, no
 // sums 416; part of the exponentials as polynomials on the fma pipe 430 at best.
+// The step from there to 335 was the queries, which a row per lane fetched from L2
+// several times over, and the weight of an item's start in the division of work.
 // Two score buffers of 64 positions per tile let the tensor cores run while the
 // softmax works on the other.
 //
@@ -55,7 +57,10 @@ static_assert(2 * REGS_SOFTMAX + 2 * REGS_CONVERT + REGS_ISSUE <= 5 * 96, "regis
 constexpr int TK = 64;      // positions per block
 constexpr int STAGES = 4;   // blocks of keys and of values in shared memory
 constexpr int SCALES = 8;   // blocks whose scales are kept
-constexpr int START = 4;    // units an item's queries and results count
+// Units that an item's queries, its first blocks' growing maxima and its results
+// count, so that CTAs with many items end with the others (two prompt chunks: 354
+// us with 4, 343 with 8, 335 with 11, 338 with 14).
+constexpr int START = 11;
 
 // An item's (sequence, row tile) and how many blocks it has.
 struct Item {
@@ -187,6 +192,10 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
                : "memory");
 }
 
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
 struct TcArgs {
   int64_t ldq;
   int heads, G, most_r;  // query heads, heads per kv head, row tiles of the longest sequence
@@ -195,6 +204,100 @@ struct TcArgs {
   float* part_ml;   // [2 W][ROWS][2]
   Cut* cuts;        // [W] the items that the runs' starts cut
 };
+
+// Stages 32 rows of queries, row0 and on of the item's `total`, at dst (rows of 128
+// bytes, planes of 64 elements `plane` bytes apart), and gives lane i row i's factor
+// back.  D / 8 lanes share a row (a row per lane fetched every sector several times:
+// a megabyte from L2 for 256 rows), each with two runs of four elements that rotate
+// with one another, so that four rows' loads are on their way in 48 registers.
+// Rounded as rotated8.  `parity` >= 0: only every second group of rows is written.
+// TWO: `term` 1 writes what the rounding to f16 left.
+template <typename TQ, int D, bool TWO>
+__device__ __forceinline__ void stage_queries(const TQ* __restrict__ Q, const TcArgs& ar,
+                                              const Rope& rp, const Item& it, int row0, int total,
+                                              uint32_t dst, int plane, int parity, int term,
+                                              float& fq, int* status) {
+  constexpr int P = D / 8, RPP = 32 / P, BATCH = 4;
+  const int lane = threadIdx.x & 31, p = lane % P, sub = lane / P;
+  const int half = rp.rot >> 1;
+  const bool turns = rp.max_pos > 0 && 8 * p < rp.rot, split = turns && !rp.interleaved;
+  const int e0 = split ? 4 * p : 8 * p, e1 = split ? e0 + half : e0 + 4;
+  const TQ* q0 = Q + int64_t(it.q0) * ar.ldq + int64_t(it.h) * ar.G * D;
+  const uint32_t d0 = dst + (e0 / 64) * plane + (e0 & 4) * 2, d1 = dst + (e1 / 64) * plane + (e1 & 4) * 2;
+#pragma unroll 1
+  for (int s0 = 0; s0 < P; s0 += BATCH) {
+    uint2 lo[BATCH], hi[BATCH];
+    float4 c[BATCH], sn[BATCH];
+    uint32_t plain = 0;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int qr = row0 + (s0 + k) * RPP + sub;
+      const int row = qr < total ? qr : total - 1;  // (rows behind the last become zeros)
+      const int i = row / ar.G, pos = it.len - it.n + i;
+      const TQ* src = q0 + int64_t(i) * ar.ldq + (row - i * ar.G) * D;
+      lo[k] = __ldg(reinterpret_cast<const uint2*>(src + e0));
+      hi[k] = __ldg(reinterpret_cast<const uint2*>(src + e1));
+      c[k] = make_float4(1.f, 1.f, 1.f, 1.f), sn[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rp.cos != nullptr && pos >= rp.max_pos) record_error(status, WQ_ERR_ARG);
+      if (!turns || pos < 0 || pos >= rp.max_pos) {
+        plain |= 1u << k;
+      } else {
+        c[k] = __ldg(reinterpret_cast<const float4*>(rp.cos + int64_t(pos) * half + 4 * p));
+        sn[k] = __ldg(reinterpret_cast<const float4*>(rp.sin + int64_t(pos) * half + 4 * p));
+      }
+      if (qr >= total) lo[k] = hi[k] = make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      float v[8];
+      unpack2<TQ>(lo[k].x, v[0], v[1]);
+      unpack2<TQ>(lo[k].y, v[2], v[3]);
+      unpack2<TQ>(hi[k].x, v[4], v[5]);
+      unpack2<TQ>(hi[k].y, v[6], v[7]);
+      if (!(plain >> k & 1)) {
+        const float cc[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+        const float ss[4] = {sn[k].x, sn[k].y, sn[k].z, sn[k].w};
+        // pair e: elements e and e + 4 of the eight, or 2 e and 2 e + 1
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = split ? v[e] : v[2 * e], b = split ? v[4 + e] : v[2 * e + 1];
+          x[e] = __fsub_rn(__fmul_rn(a, cc[e]), __fmul_rn(b, ss[e]));
+          x[4 + e] = __fadd_rn(__fmul_rn(b, cc[e]), __fmul_rn(a, ss[e]));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = split ? x[e] : x[(e & 1) * 4 + (e >> 1)];
+      }
+      float a = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+#pragma unroll
+      for (int o = P / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      // a power of two brings the row's largest element to [2^14, 2^15)
+      int ex = (a > 0.f && a <= 3.4028234663852886e38f) ? 141 - int(__float_as_uint(a) >> 23) : 0;
+      ex = ex > 100 ? 100 : ex;
+      const float up = __uint_as_float(uint32_t(127 + ex) << 23);
+      const int s = s0 + k;
+      const float back = __shfl_sync(0xffffffffu, __uint_as_float(uint32_t(127 - ex) << 23),
+                                     (lane % RPP) * P);
+      if (lane / RPP == s) fq = back;
+      if (parity >= 0 && (s & 1) != parity) continue;
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y = v[2 * e] * up, z = v[2 * e + 1] * up;
+        if (TWO && term == 1) {
+          y -= __half2float(__float2half_rn(y));
+          z -= __half2float(__float2half_rn(z));
+        }
+        h[e] = f16x2(y, z);
+      }
+      const int w = s * RPP + sub;
+      sts64(d0 + w * 128 + ((((e0 & 63) >> 3) ^ (w & 7)) << 4), h[0], h[1]);
+      sts64(d1 + w * 128 + ((((e1 & 63) >> 3) ^ (w & 7)) << 4), h[2], h[3]);
+    }
+  }
+}
 
 template <typename TQ, int FMT, int D, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -328,50 +431,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int pos = it.len - it.n + i;
       // (a row of no query takes part as zeros, and asks for no masking)
       const int lim = live ? min(it.len, pos + 1) : 0x7fffffff;
-      // -------- this row of queries, as f16 in the swizzled operand layout
-      float fq;
+      // -------- the warp's 32 rows of queries, as f16 in the swizzled operand layout
+      float fq = 0.f;
       {
-        const TQ* src = Q + int64_t(it.q0 + i) * ar.ldq + int64_t(it.h * ar.G + (rr - i * ar.G)) * D;
-        Rope rq = rp;
-        if (pos < 0 || (rq.cos != nullptr && pos >= rq.max_pos)) {
-          if (pos >= 0 && live) record_error(status, WQ_ERR_ARG);
-          rq.cos = nullptr;
-        }
-        float a = 0.f;
-        if (live)
-#pragma unroll 4
-          for (int d = 0; d < D; d += 8) {
-            float v[8];
-            rotated8(src, d, pos, rq, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
-          }
-        // a power of two brings the row's largest element to [2^14, 2^15)
-        int ex = (a > 0.f && a <= 3.4028234663852886e38f) ? 141 - int(__float_as_uint(a) >> 23) : 0;
-        ex = ex > 100 ? 100 : ex;
-        const float up = __uint_as_float(uint32_t(127 + ex) << 23);
-        fq = __uint_as_float(uint32_t(127 - ex) << 23) * ar.scale_log2;
-        // one term: with shared rows each group of warps writes half of it;
-        // two terms: group 0 the rounded query, group 1 what that left
-        const int d0 = !PAIR && !TWO ? x * (D / 2) : 0, d1 = !PAIR && !TWO ? d0 + D / 2 : D;
-        const uint32_t dst = qs + ((PAIR || TWO) ? x * S::TILE : 0) + row * 128;
-#pragma unroll 2
-        for (int d = d0; d < d1; d += 8) {
-          float v[8] = {};
-          if (live) rotated8(src, d, pos, rq, v);
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p = v[2 * e] * up, q = v[2 * e + 1] * up;
-            if (TWO && x == 1) {
-              p -= __half2float(__float2half_rn(p));
-              q -= __half2float(__float2half_rn(q));
-            }
-            h[e] = f16x2(p, q);
-          }
-          sts128(dst + (d / 64) * PLANE + ((((d & 63) >> 3) ^ (row & 7)) << 4), h[0], h[1], h[2],
-                 h[3]);
-        }
+        const uint32_t dst = qs + ((PAIR || TWO) ? x * S::TILE : 0) + (warp & 3) * 32 * 128;
+        const int row0 = it.r * ROWS + (PAIR ? x * 128 : 0) + (warp & 3) * 32;
+        // with one tile of one term each group of warps writes half of it; two terms:
+        // group 0 the rounded query, group 1 what that left
+        const int parity = !PAIR && !TWO ? x : -1;
+        stage_queries<TQ, D, TWO>(Q, ar, rp, it, row0, it.n * ar.G, dst, PLANE, parity, x, fq,
+                                  status);
+        fq *= ar.scale_log2;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.qfull);
