@@ -22,15 +22,16 @@
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
 // Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
-// all (E4M3): 335 us, 702 TFLOP/s of products.  Bound by the hand-offs: a
+// all (E4M3): 308 us, 763 TFLOP/s of products.  Bound by the hand-offs: a
 // block takes a tile 2600 cycles on average, of which its two products are 690
-// (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value step of
-// each tile) and its exponentials 512 of the special-function units.  Leaving one
+// (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value
+// step) and its exponentials 512 of the special-function units.  Leaving one
 // part out at a time, at 431 us, says that none of them is the limit by itself: no
 // exponentials 399 us, no converter stores 419, no converter loads either 409, no
 // sums 416; part of the exponentials as polynomials on the fma pipe 430 at best.
-// The step from there to 335 was the queries, which a row per lane fetched from L2
-// several times over, and the weight of an item's start in the division of work.
+// The steps from there to 308 were the queries, which a row per lane fetched from L2
+// several times over, the weight of an item's start in the division of work, and a
+// wait per block less (a wait that is over already costs 150 cycles).
 // Two score buffers of 64 positions per tile let the tensor cores run while the
 // softmax works on the other.
 //
@@ -130,8 +131,10 @@ struct Smem {
     // per tile: two rounds in turn (a wait tells a round from the one two before,
     // which is known to be over, but not from the one in between)
     uint64_t sfull[2][2], pfull[2][2], odone[2][2];
-    uint64_t scfull[SCALES], mfull, mfree, drain[2];
-    // per block and 16 positions: ks, log2 vs, 1 / vs.  A slot is written again 8
+    uint64_t mfull, mfree, drain[2];
+    // per block and 16 positions: ks, log2 vs, 1 / vs, written before the block's
+    // keys are announced, read after the scores that waited for them are (a barrier
+    // of their own cost the softmax 150 cycles a block).  A slot is written again 8
     // blocks later, when the scores 4 blocks later are done, whose predecessors 2
     // blocks back have been through the softmax.
     float4 scale[SCALES][TK / 16];
@@ -380,7 +383,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc::mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < SCALES; ++i) tc::mbar_init(&sm.scfull[i], 1);
     tc::mbar_init(&sm.mfull, 4);
     tc::mbar_init(&sm.mfree, 4);
     tc::mbar_init(&sm.qfull, 8);
@@ -453,9 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
         const uint32_t b = block + uint32_t(j);
         const uint32_t buf = op & 1u, st = st0 + buf * TK;
-        if (!(ok = tc::wait_warp(&sm.sfull[x][buf], (op >> 1) & 1u, wd) &&
-                   tc::wait_warp(&sm.scfull[b % SCALES], (b / SCALES) & 1u, wd)))
-          break;
+        if (!(ok = tc::wait_warp(&sm.sfull[x][buf], (op >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
         const int tok0 = (t0 + j) * TK;
         const float4* scl = sm.scale[b % SCALES];
@@ -724,8 +724,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             sm.scale[block % SCALES][lane] =
                 make_float4(fmaxf(ks, 1e-30f), vs < 0.f ? -CUDART_INF_F : __log2f(v),
                             vs < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.scfull[block % SCALES]);
         }
         store(w, region + s * S::BLOCK);
         if (lane == 0) tc::mbar_arrive(&full[s]);
