@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m = -CUDART_INF_F, l = 0.f;
       const int t0 = place.t0, J = place.t1 - t0;
       int done = 0;  // of this tile in this segment
+      bool seen = false;  // the block's scores were complete when the last one's weights were
       for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
         const uint32_t b = block + uint32_t(j);
         const uint32_t buf = op & 1u, st = st0 + buf * TK;
-        if (!(ok = tc::wait_warp(&sm.sfull[x][buf], (op >> 1) & 1u, wd))) break;
+        if (!seen && !(ok = tc::wait_warp(&sm.sfull[x][buf], (op >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
         const int tok0 = (t0 + j) * TK;
         const float4* scl = sm.scale[b % SCALES];
@@ -528,11 +529,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok) break;
         l += sum;
+        seen = j + (PAIR ? 1 : 2) < J &&
+               tc::mbar_test(&sm.sfull[x][(op + 1) & 1u], ((op + 1) >> 1) & 1u);
         tc::tmem_st_x32(st, p);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_relaxed(&sm.pfull[x][buf]);
+        seen = __all_sync(0xffffffffu, seen);
       }
       if (!ok) break;
       if (done) {
@@ -754,9 +758,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
       tc::fence_after_sync();
       const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
+      auto keys = [&](int i) {
+        const uint32_t b = block + (PAIR ? i : 2 * i + x);
+        return tc::wait_warp(&sm.kfull[b % STAGES], (b / STAGES) & 1u, wd);
+      };
       auto scores = [&](int i) {
         const uint32_t b = block + (PAIR ? i : 2 * i + x), s = b % STAGES, buf = sc & 1u;
-        if (!tc::wait_warp(&sm.kfull[s], (b / STAGES) & 1u, wd)) return false;
         tc::fence_after_sync();
         ++sc;
         const uint64_t dk = tc::sdesc_k_sw128(ksm + s * S::BLOCK);
@@ -774,13 +781,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::mma_commit(&sm.kempty[s]);
         }
         __syncwarp();
-        return true;
       };
       // the scores are two rounds ahead of their weights
-      for (int i = 0; i < 2 && i < N && ok; ++i) ok = scores(i);
+      for (int i = 0; i < 2 && i < N && ok; ++i)
+        if ((ok = keys(i))) scores(i);
       for (int i = 0; i < N && ok; ++i) {
         const uint32_t b = block + (PAIR ? i : 2 * i + x), s = b % STAGES, buf = pv & 1u;
+        // (the weights last: what follows them is what the softmax waits for)
         if (!(ok = tc::wait_warp(&sm.vfull[s], (b / STAGES) & 1u, wd))) break;
+        if (i + 2 < N && !(ok = keys(i + 2))) break;
         if (!(ok = tc::wait_warp(&sm.pfull[x][buf], (pv >> 1) & 1u, wd))) break;
         ++pv;
         tc::fence_after_sync();
@@ -794,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::mma_commit(&sm.vempty[s]);
         }
         __syncwarp();
-        if (i + 2 < N) ok = scores(i + 2);
+        if (i + 2 < N) scores(i + 2);
       }
       block += J;
     }
