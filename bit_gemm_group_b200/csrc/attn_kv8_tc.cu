@@ -22,16 +22,17 @@
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
 // Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
-// all (E4M3): 308 us, 763 TFLOP/s of products.  Bound by the hand-offs: a
-// block takes a tile 2600 cycles on average, of which its two products are 690
+// all (E4M3): 302 us, 779 TFLOP/s of products.  Bound by the hand-offs: a
+// block took a tile 2600 cycles at 431 us, of which its two products are 690
 // (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value
 // step) and its exponentials 512 of the special-function units.  Leaving one
 // part out at a time, at 431 us, says that none of them is the limit by itself: no
 // exponentials 399 us, no converter stores 419, no converter loads either 409, no
 // sums 416; part of the exponentials as polynomials on the fma pipe 430 at best.
-// The steps from there to 308 were the queries, which a row per lane fetched from L2
-// several times over, the weight of an item's start in the division of work, and a
-// wait per block less (a wait that is over already costs 150 cycles).
+// The steps from there to 302 were the queries, which a row per lane fetched from L2
+// several times over, the weight of an item's start in the division of work, and
+// waits (one that is over already costs 150 cycles): one less per block, the others
+// where nothing waits for them.
 // Two score buffers of 64 positions per tile let the tensor cores run while the
 // softmax works on the other.
 //
@@ -60,7 +61,8 @@ constexpr int STAGES = 4;   // blocks of keys and of values in shared memory
 constexpr int SCALES = 8;   // blocks whose scales are kept
 // Units that an item's queries, its first blocks' growing maxima and its results
 // count, so that CTAs with many items end with the others (two prompt chunks: 354
-// us with 4, 343 with 8, 335 with 11, 338 with 14).
+// us with 4, 343 with 8, 335 with 11, 338 with 14; 36 rows over 2 x 4096 45 us with
+// 4, 38 with 7 and with 11).
 constexpr int START = 11;
 
 // An item's (sequence, row tile) and how many blocks it has.
@@ -934,15 +936,17 @@ int launch_tc_by_type(const void* Q, int dtype, int64_t ldq, int64_t heads, cons
 // Whether the tensor-memory kernel takes the call: more than 32 rows to a
 // (sequence, kv head).  The other kernel reads the codes once for each 8 rows, this
 // one once for 128 (its time hardly depends on the rows).  Measured, the other and
-// this, over 4 x 32768 positions of 8 kv heads of 128: 16 rows 116 and 182 us, 24
-// 165 and 182, 32 199 and 182, 40 235 and 184, 64 363 and 186; over 64 x 2048 32
-// rows 207 and 207; heads of 64, 32 rows 135 and 145, 40 165 and 147.  Results of
+// this, over 4 x 32768 positions of 8 kv heads of 128: 16 rows 117 and 176 us, 24
+// 163 and 176, 32 198 and 176, 40 235 and 176, 64 363 and 178; over 64 x 2048 32
+// rows 206 and 215, 40 247 and 217; heads of 64, 32 rows 135 and 141, 40 165 and
+// 141; over 4 x 1024 40 rows 29 and 33.  Results of
 // 256 elements for two tiles do not fit in tensor memory beside the scores.
 bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
   return D <= 128 && max_q * (heads / kv_heads) > 32;
 }
-// Two row tiles that share the converted blocks: where there are two (160 rows over
-// 4 x 32768: 223 us, and 336 one tile after the other), and the queries are one term.
+// Two row tiles that share the converted blocks: where there are two, and the queries
+// are one term (160 rows over 4 x 32768: 223 us, and 336 one tile after the other; two
+// terms of two tiles do not fit in shared memory beside the blocks).
 bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
   return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
 }
