@@ -568,8 +568,11 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
   p.counters = p.sx + up256(size_t(kb * p.mp) * 4);
   p.tiles = p.nt ? int(((N + 127) / 128) * ((M + p.nt - 1) / p.nt)) : 0;
   p.n_counters = p.tiles * (p.nt > 64 ? 8 : 4);  // one for each adding warp
-  p.partials = p.counters + up256(size_t(p.n_counters) * 4);
-  p.bytes = p.partials + (p.nt ? size_t(sm_count()) * 2 * p.nt * 128 * 4 : 0);
+  // room for the split kernel whether it is taken or not, so that the size grows
+  // with M and a workspace serves fewer tokens too
+  const int64_t most = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  p.partials = p.counters + up256(size_t((N + 127) / 128) * size_t(p.mp / 128) * 8 * 4);
+  p.bytes = p.partials + size_t(sm_count()) * 2 * size_t(most) * 128 * 4;
   return p;
 }
 

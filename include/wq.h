@@ -347,8 +347,9 @@ WQ_API int wq_kv8_append(const void *K, const void *V, int dtype, int64_t n, int
  * Codes and scales of positions that a row does not see, and bytes of slots
  * nobody wrote, do not reach its result.
  * ws: wq_attn_kv8_workspace_bytes(...) bytes on the current device, 256-byte
- * aligned, any contents; calls that may overlap on the GPU need separate
- * workspaces.  Results do not depend on timing.
+ * aligned, any contents (a workspace for max_new serves fewer as well); calls
+ * that may overlap on the GPU need separate workspaces.  Results do not depend
+ * on timing.
  */
 WQ_API size_t wq_attn_kv8_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
                                           int64_t max_new);
@@ -438,8 +439,9 @@ WQ_API int wq_quantize_fp8_block(const void *A, int a_dtype, int64_t R, int64_t 
  * byte once with the work split evenly over the SMs.  Results do not depend
  * on timing (partial sums are joined in a fixed order).  Requires K % 16 == 0
  * and N % 8 == 0.  ws: wq_fp8_block_workspace_bytes(M, N, K) bytes on the
- * current device, 256-byte aligned, any contents; calls that may overlap on
- * the GPU need separate workspaces.
+ * current device, 256-byte aligned, any contents; a workspace for M tokens
+ * serves fewer as well; calls that may overlap on the GPU need separate
+ * workspaces.
  */
 WQ_API size_t wq_fp8_block_workspace_bytes(int64_t M, int64_t N, int64_t K);
 WQ_API int wq_gemm_fp8_block(const void *X, int64_t M, int64_t K, const void *Wq,

@@ -127,3 +127,13 @@ def test_shared_argument_checks():
     ]:
         with pytest.raises(wq.WQError, match=text):
             wq._kv8_args(**{**ok, **change})
+
+
+@pytest.mark.parametrize("N,K", [(256, 512), (2048, 4096), (28672, 8192), (64, 11008)])
+def test_workspaces_serve_fewer_rows(N, K):
+    sizes = [wq.wq_fp8_block_workspace_bytes(M, N, K)
+             for M in (1, 16, 17, 32, 33, 64, 65, 128, 129, 300, 1000, 5000)]
+    assert sizes == sorted(sizes)
+    for D in (64, 128, 256):
+        sizes = [wq.wq_attn_kv8_workspace_bytes(4, 32, 8, D, n) for n in (1, 2, 8, 9, 32, 33, 4096)]
+        assert sizes == sorted(sizes)
