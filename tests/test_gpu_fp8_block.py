@@ -156,3 +156,16 @@ def test_block_scales_beat_row_scales_on_outliers():
     fw, fs = wq.quantize_fp8_rows(W.cuda())
     er = (wq.gemm_fp8(X.cuda(), fw, fs).double().cpu() - ref).norm()
     assert eb < er
+
+
+def test_gemm_around_the_choice_of_kernel_with_one_workspace():
+    # few K blocks take the large kernel from 33 tokens on, many the split one; a workspace for
+    # the most tokens serves all of them
+    for N, K in ((392, 1040), (392, 8208)):
+        W = torch.randn(N, K, device="cuda").to(torch.bfloat16)
+        qw, sw = wq.quantize_fp8_block(W, 128)
+        ws = torch.empty(wq.wq_fp8_block_workspace_bytes(300, N, K), dtype=torch.uint8,
+                         device="cuda").fill_(255)
+        for M in (300, 129, 128, 96, 65, 64, 33, 32, 1):
+            X = torch.randn(M, K, device="cuda").to(torch.bfloat16)
+            check_product(X.cpu(), W, wq.gemm_fp8_block(X, qw, sw, ws=ws), qw, sw)
