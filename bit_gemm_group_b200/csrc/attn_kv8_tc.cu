@@ -88,6 +88,11 @@ struct Item {
     tiles = seen > 0 ? (seen + TK - 1) / TK : 1;
   }
   __device__ __forceinline__ bool valid() const { return n > 0 && r < R; }
+  // the first position that not every query of the row tile sees
+  __device__ __forceinline__ int first_hidden(int G, int rows) const {
+    const int seen = len - n + int(int64_t(r) * rows / G) + 1;
+    return seen < 0 ? 0 : seen < len ? seen : len;
+  }
 };
 
 // Walks over the work of a CTA's run: the item and its blocks [t0, t1).
@@ -146,6 +151,10 @@ struct Smem {
     // memory comes back from L2 here)
     Walk walk[WARPS];
     int start_p, tmem_base, abort_flag;
+    // set by the converters of values: a code that is no number where the rows of an
+    // item differ in what they see (written before the block is announced, read after
+    // its product is done)
+    volatile int nans;
   };
   static constexpr size_t BYTES = 1024 + BLOCKS + sizeof(Ctrl);
 };
@@ -389,6 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::mbar_init(&sm.mfree, 4);
     tc::mbar_init(&sm.qfull, 8);
     sm.abort_flag = 0;
+    sm.nans = 0;
     tc::fence_mbar_init();
   }
   if (warp == 16) {
@@ -575,6 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + it.h * ar.G + (rr - i * ar.G)) * D;
         float* pd = ar.parts + (part * ROWS + prow) * D;
+        const bool nans = FMT == WQ_W8_E4M3 && live && sm.nans != 0;
         if (!whole) {
           __stcg(ar.part_ml + (part * ROWS + prow) * 2, m);
           __stcg(ar.part_ml + (part * ROWS + prow) * 2 + 1, l);
@@ -590,6 +601,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 16; ++e) {
             v[e] = __uint_as_float(a[e]) * w0;
             if (both) v[e] = fmaf(__uint_as_float(b[e]), w1, v[e]);
+          }
+          if (nans) {
+            const int end = min(lim, place.t1 * TK);
+#pragma unroll 1
+            for (int p = max(t0, it.first_hidden(ar.G, ROWS) / TK) * TK; p < end; ++p) {
+              const int page = __ldg(bt.table + int64_t(it.b) * bt.width + (p >> c.tshift));
+              if (page < 0 || page >= c.pages) continue;
+              const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+                  c.vq + ((c.block(page, it.h) << c.tshift) + (p & (T_ - 1))) * D + q * 16));
+              const uint32_t n4[4] = {e4m3_nans(w.x), e4m3_nans(w.y), e4m3_nans(w.z), e4m3_nans(w.w)};
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (n4[e / 4] >> (8 * (e & 3)) & 0x80u) v[e] = CUDART_NAN_F;
+            }
           }
           if (!whole) {
 #pragma unroll
@@ -647,6 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (; more && ok; more = step()) {
       const int t0 = place.t0, J = place.t1 - t0, len = it.len;
+      const int hidden = FMT == WQ_W8_E4M3 && values ? it.first_hidden(ar.G, ROWS) : len;
       // Lane g of a warp looks after positions 16 g to 16 g + 15 of a block (one
       // page): table entry two blocks ahead, address and (first warp) scales one
       // block ahead, so that nothing here waits for the load before it.
@@ -730,6 +756,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             sm.scale[block % SCALES][lane] =
                 make_float4(fmaxf(ks, 1e-30f), vs < 0.f ? -CUDART_INF_F : __log2f(v),
                             vs < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
+        }
+        if (hidden < len && (t0 + j + 1) * TK > hidden) {
+          uint32_t any = 0;
+          auto clean = [&](uint32_t& x) {
+            const uint32_t b = e4m3_nans(x);
+            any |= b;
+            x = without(x, b);
+          };
+#pragma unroll
+          for (int i = 0; i < N; ++i) clean(w[i].x), clean(w[i].y), clean(w[i].z), clean(w[i].w);
+          if (any) sm.nans = 1;
         }
         store(w, region + s * S::BLOCK);
         if (lane == 0) tc::mbar_arrive(&full[s]);

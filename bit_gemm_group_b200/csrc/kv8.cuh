@@ -113,6 +113,19 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// 0x80 in each byte of a word that is an E4M3 NaN (0x7F or 0xFF).  The products
+// multiply a weight of 0 by every value of a block that some row sees only in part,
+// and 0 NaN is no 0: there NaN codes are taken as 0, and the rows that do see one
+// are given their NaN at the end (a look at the codes again, for caches that hold
+// one only).
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+// The word with its NaN codes, as e4m3_nans marks them, zeroed.
+__device__ __forceinline__ uint32_t without(uint32_t w, uint32_t nans) {
+  return w & ~((nans >> 7) * 0xFFu);
+}
+
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
