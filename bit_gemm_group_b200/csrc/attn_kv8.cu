@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
       const float ks = lds32f(scb + 8 * k), vs = lds32f(scb + 8 * k + 4);
       const float v = fmaxf(vs, 1e-30f);
       f = fq * ks;
-      lv = vs < 0.f ? -CUDART_INF_F : __log2f(v);
+      lv = vs < 0.f ? -CUDART_INF_F : __log2f(vs < 1e-30f ? 1e-30f : vs);  // (NaN stays)
       rv = __fdividef(1.f, v);
     };
     float f0, lv0, rv0, f1, lv1, rv1;

@@ -151,9 +151,9 @@ struct Smem {
     // memory comes back from L2 here)
     Walk walk[WARPS];
     int start_p, tmem_base, abort_flag;
-    // set by the converters of values: a code that is no number where the rows of an
-    // item differ in what they see (written before the block is announced, read after
-    // its product is done)
+    // set by the converters: a value's code or a scale that is no number where the rows
+    // of an item differ in what they see (written before the block is announced, read
+    // after its product is done)
     volatile int nans;
   };
   static constexpr size_t BYTES = 1024 + BLOCKS + sizeof(Ctrl);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + it.h * ar.G + (rr - i * ar.G)) * D;
         float* pd = ar.parts + (part * ROWS + prow) * D;
-        const bool nans = FMT == WQ_W8_E4M3 && live && sm.nans != 0;
+        const bool nans = live && sm.nans != 0;
         if (!whole) {
           __stcg(ar.part_ml + (part * ROWS + prow) * 2, m);
           __stcg(ar.part_ml + (part * ROWS + prow) * 2 + 1, l);
@@ -608,12 +608,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int p = max(t0, it.first_hidden(ar.G, ROWS) / TK) * TK; p < end; ++p) {
               const int page = __ldg(bt.table + int64_t(it.b) * bt.width + (p >> c.tshift));
               if (page < 0 || page >= c.pages) continue;
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-                  c.vq + ((c.block(page, it.h) << c.tshift) + (p & (T_ - 1))) * D + q * 16));
-              const uint32_t n4[4] = {e4m3_nans(w.x), e4m3_nans(w.y), e4m3_nans(w.z), e4m3_nans(w.w)};
+              const int64_t blk = c.block(page, it.h);
+              const float ks = __ldg(c.ks + blk), vs = __ldg(c.vs + blk);
+              uint4 n4 = make_uint4(0, 0, 0, 0);
+              if (ks != ks || !(vs <= 3.4028234663852886e38f)) {
+                n4 = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+              } else if (FMT == WQ_W8_E4M3) {
+                n4 = __ldg(reinterpret_cast<const uint4*>(
+                    c.vq + ((blk << c.tshift) + (p & (T_ - 1))) * D + q * 16));
+                n4 = make_uint4(e4m3_nans(n4.x), e4m3_nans(n4.y), e4m3_nans(n4.z), e4m3_nans(n4.w));
+              }
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (n4[e / 4] >> (8 * (e & 3)) & 0x80u) v[e] = CUDART_NAN_F;
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t w = e < 4 ? n4.x : e < 8 ? n4.y : e < 12 ? n4.z : n4.w;
+                if (w >> (8 * (e & 3)) & 0x80u) v[e] = CUDART_NAN_F;
+              }
             }
           }
           if (!whole) {
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (; more && ok; more = step()) {
       const int t0 = place.t0, J = place.t1 - t0, len = it.len;
-      const int hidden = FMT == WQ_W8_E4M3 && values ? it.first_hidden(ar.G, ROWS) : len;
+      const int hidden = it.first_hidden(ar.G, ROWS);
       // Lane g of a warp looks after positions 16 g to 16 g + 15 of a block (one
       // page): table entry two blocks ahead, address and (first warp) scales one
       // block ahead, so that nothing here waits for the load before it.
@@ -751,13 +760,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t s = block % STAGES;
         if (!(ok = tc::wait_warp(&empty[s], ((block / STAGES) & 1u) ^ 1u, wd))) return;
         if (warp == 8) {
+          // A key scale that is no number or a value scale that is not finite makes the
+          // rows that see it NaN: here, or at the end where some rows do not see it.
+          const bool odd = ks != ks || !(vs <= 3.4028234663852886e38f);
+          const bool skip = vs < 0.f || (odd && (t0 + j + 1) * TK > hidden);
           const float v = fmaxf(vs, 1e-30f);
           if (lane < TK / 16)
             sm.scale[block % SCALES][lane] =
-                make_float4(fmaxf(ks, 1e-30f), vs < 0.f ? -CUDART_INF_F : __log2f(v),
-                            vs < 0.f ? 0.f : __fdividef(1.f, v), 0.f);
+                make_float4(fmaxf(ks, 1e-30f),
+                            skip ? -CUDART_INF_F : odd ? CUDART_NAN_F : __log2f(v),
+                            skip ? 0.f : __fdividef(1.f, v), 0.f);
+          if (odd && skip) sm.nans = 1;
         }
-        if (hidden < len && (t0 + j + 1) * TK > hidden) {
+        if (FMT == WQ_W8_E4M3 && values && (t0 + j + 1) * TK > hidden) {
           uint32_t any = 0;
           auto clean = [&](uint32_t& x) {
             const uint32_t b = e4m3_nans(x);

@@ -1,5 +1,5 @@
 """What a row of a call does not see does not reach it, whatever the cache holds there:
-E4M3 codes that are no number.  Rows that do see them show it."""
+E4M3 codes that are no number, scales that are not finite.  Rows that do see them show it."""
 import pytest
 import torch
 
@@ -8,9 +8,9 @@ import kv8_plain as plain
 
 pytestmark = pytest.mark.gpu
 
-E4 = torch.uint8
+I8, E4 = torch.int8, torch.uint8
 BF, HF = torch.bfloat16, torch.float16
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(autouse=True)
@@ -94,3 +94,26 @@ def test_key_codes_that_are_no_number(case):
         d["cache"][0][int(st["table"][b, p // T]), p % kv, p % T, 5] = 0x7F
         want[seen(st, b, p):int(st["cu"][b + 1]), p % kv * G:p % kv * G + G] = NAN
     assert same(attend().cpu(), want)
+
+
+@pytest.mark.parametrize("code", [I8, E4])
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("which", [1, 3])
+@pytest.mark.parametrize("case", [c for c in CASES if any((L - n) // c[1] != (L - 1) // c[1]
+                                                         for n, L in c[5])])
+def test_scales_that_are_not_finite(case, which, bad, code):
+    """The scale of a sequence's last page: rows that end before it keep their bits.  Rows
+    that see it are not finite (an infinite key scale makes a score of either sign)."""
+    st, d, attend = state(case, code, seed=5)
+    D, T, kv, G, _, seqs = case
+    want = attend().cpu()
+    hit = torch.zeros(want.shape[0], dtype=torch.bool)
+    for b, (n, L) in enumerate(seqs):
+        if (L - n) // T == (L - 1) // T:
+            continue
+        d["cache"][which][int(st["table"][b, (L - 1) // T])] = bad
+        hit[seen(st, b, (L - 1) // T * T):int(st["cu"][b + 1])] = True
+    out = attend().cpu()
+    assert torch.equal(out[~hit], want[~hit])
+    if which == 3 or bad != bad:
+        assert not bool(out[hit].isfinite().any())
