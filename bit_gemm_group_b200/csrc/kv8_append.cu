@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(512)
     }
   }
   if (bad) {
-    const float top = s * TOP;
+    // (s TOP may round above the largest number)
+    const float top = fminf(s * TOP, 3.4028234663852886e38f);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
 #pragma unroll
