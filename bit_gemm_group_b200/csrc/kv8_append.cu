@@ -60,8 +60,10 @@ __global__ void __launch_bounds__(512)
     return;
   }
   const int col = (start >> c.tshift) + j;
-  const int p0 = max(start, col << c.tshift), p1 = min(len, (col + 1) << c.tshift);
-  if (p0 >= p1) return;
+  // (in 64 bits: the end of a page near 2^31 is no int)
+  const int64_t begin = int64_t(col) << c.tshift;
+  if (begin >= len) return;
+  const int p0 = max(start, int(begin)), p1 = int(min(int64_t(len), begin + T_));
   const int64_t page = col < bt.width ? __ldg(bt.table + int64_t(b) * bt.width + col) : -1;
   if (page < 0 || page >= c.pages || (rp.cos != nullptr && p1 > rp.max_pos)) {
     if (threadIdx.x == 0) record_error(status, WQ_ERR_ARG);
