@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(512)
   }
   // (a finite element is within half a unit of s TOP's last place, whose code is TOP)
   const float inv = __frcp_rn(s);
-  const uint64_t minus = two(-s, -s), inv2 = two(inv, inv);
+  const uint64_t s2 = two(s, s), minus_inv = two(-inv, -inv);
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int r = first + i * rstep;
@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(512)
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint64_t v[2] = {quot_rn_two(x[i][2 * k], minus, inv2),
-                       quot_rn_two(x[i][2 * k + 1], minus, inv2)};
+      uint64_t v[2] = {minus_quot_rn_two(x[i][2 * k], s2, minus_inv),
+                       minus_quot_rn_two(x[i][2 * k + 1], s2, minus_inv)};
       float f[4];
       if (FMT == WQ_W8_INT8) {
-        // the low byte of v + 1.5 2^23 is v rounded half to even
-        const uint64_t magic = two(12582912.f, 12582912.f);
-        v[0] = add_two(v[0], magic);
-        v[1] = add_two(v[1], magic);
+        // the low byte of 1.5 2^23 - v is -v rounded half to even
+        const uint64_t magic = two(12582912.f, 12582912.f), minus_one = two(-1.f, -1.f);
+        v[0] = fma_two(v[0], minus_one, magic);
+        v[1] = fma_two(v[1], minus_one, magic);
       }
       split_two(v[0], f[0], f[1]);
       split_two(v[1], f[2], f[3]);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(512)
       } else {
         const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
         const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
-        o[k] = a | (b << 16);
+        o[k] = (a | (b << 16)) ^ 0x80808080u;
       }
     }
     uint8_t* dst = codes + int64_t(slot0 + r) * D;

@@ -83,10 +83,12 @@ __device__ __forceinline__ float quot_e4m3(float x, float s, float inv) {
 // 0 either way).  Five instructions of the fma pipe, where deciding only the
 // quotients near half-way costs more on the half-rate integer pipe: two 16-bit
 // floats often have a quotient that is a tie of the 8-bit grid.
+// The remainder is taken as q s - x, so that a zero keeps its sign: (-0) s - (-0) is
+// +0, whose product with -y is -0 (x - q s would be +0 and q + 0 y as well).
 __device__ __forceinline__ float quot_rn(float x, float s, float y) {
   float q = x * y;
-  q = fmaf(fmaf(-q, s, x), y, q);
-  return fmaf(fmaf(-q, s, x), y, q);
+  q = fmaf(fmaf(q, s, -x), -y, q);
+  return fmaf(fmaf(q, s, -x), -y, q);
 }
 
 // Two fp32 in one register pair, with the packed instructions on them (each half
@@ -104,21 +106,18 @@ __device__ __forceinline__ uint64_t mul_two(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// quot_rn of both halves; `minus` is -s twice, y fl(1 / s) twice.
-__device__ __forceinline__ uint64_t quot_rn_two(uint64_t x, uint64_t minus, uint64_t y) {
-  uint64_t q = mul_two(x, y);
-  q = fma_two(fma_two(q, minus, x), y, q);
-  return fma_two(fma_two(q, minus, x), y, q);
+// -fl(x / s) of both halves, as quot_rn; `s2` is s twice, `minus_y` -fl(1 / s) twice.
+// (Packed operands have no sign of their own to flip: with q for -x / s the remainder x +
+// q s keeps the sign of a zero without one.)
+__device__ __forceinline__ uint64_t minus_quot_rn_two(uint64_t x, uint64_t s2, uint64_t minus_y) {
+  uint64_t q = mul_two(x, minus_y);
+  q = fma_two(fma_two(q, s2, x), minus_y, q);
+  return fma_two(fma_two(q, s2, x), minus_y, q);
 }
 
 // The largest |x| (sym) or the smallest and largest x (asym) of a lane's 16
