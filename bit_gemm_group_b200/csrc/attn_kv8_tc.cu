@@ -138,6 +138,10 @@ struct Smem {
     // per tile: two rounds in turn (a wait tells a round from the one two before,
     // which is known to be over, but not from the one in between)
     uint64_t sfull[2][2], pfull[2][2], odone[2][2];
+    // An item of one block gives tile 1's issuer no round, so that nothing else says
+    // that it has seen the item's queries: two items on, the parity of `qfull` would
+    // tell it the wrong phase.
+    uint64_t idle;
     uint64_t mfull, mfree, drain[2];
     // per block and 16 positions: ks, log2 vs, 1 / vs, written before the block's
     // keys are announced, read after the scores that waited for them are (a barrier
@@ -394,6 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc::mbar_init(&sm.drain[i], 1);
     }
+    tc::mbar_init(&sm.idle, 1);
     tc::mbar_init(&sm.mfull, 4);
     tc::mbar_init(&sm.mfree, 4);
     tc::mbar_init(&sm.qfull, 8);
@@ -438,6 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t op = 0;  // tensor-core rounds of this tile so far
     bool ok = true, first_seg = true;
     uint32_t block = 0, seg = 0;  // blocks and items of the CTA so far
+    uint32_t idles = 0;           // items without a round of this tile
     for (; more && ok; more = step(), ++seg) {
       const int rr = it.r * ROWS + (PAIR ? x * 128 : 0) + row;
       const bool live = rr < it.n * ar.G;
@@ -554,6 +560,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (done) {
         if (!(ok = tc::wait_warp(&sm.odone[x][(op - 1) & 1u], ((op - 1) >> 1) & 1u, wd))) break;
         tc::fence_after_sync();
+      } else if (!PAIR) {
+        if (!(ok = tc::wait_warp(&sm.idle, idles++ & 1u, wd))) break;
       }
       // -------- results
       const bool whole = place.t0 == 0 && place.t1 == it.tiles;
@@ -810,6 +818,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (; more && ok; more = step(), ++seg) {
       const int J = place.t1 - place.t0, N = PAIR ? J : (J + 1 - x) >> 1;
       ok = tc::wait_warp(&sm.qfull, seg & 1u, wd);
+      if (!PAIR && N == 0 && lane == 0) tc::mbar_arrive(&sm.idle);
       tc::fence_after_sync();
       const uint64_t dq = tc::sdesc_k_sw128(qs + (PAIR ? x * S::TILE : 0));
       auto keys = [&](int i) {
