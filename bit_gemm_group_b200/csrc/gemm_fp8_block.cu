@@ -468,10 +468,11 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         tc::fence_before_sync();
         __syncwarp();
         // the stage is free when every epilogue warp has read its scales and
-        // the tensor cores its tiles (they have: tfull)
+        // the tensor cores its tiles (they have: tfull).  A release: the copy that
+        // overwrites the scales comes after the warp's reads of them.
         if (lane == 0) {
           tc::mbar_arrive_relaxed(&sm.tempty[buf]);
-          tc::mbar_arrive_relaxed(&sm.empty[s]);
+          tc::mbar_arrive(&sm.empty[s]);
         }
       }
       if (!ok) break;

@@ -51,10 +51,11 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// For what a warp has read (from tensor memory: complete after tmem_wait_ld; from
-// shared memory: values in use) and nothing that it wrote: relaxed, since a release first waits for the warp's global
-// loads on their way (900 cycles of a K block's 1500 in the large block-scaled
-// product).
+// For a warp's accesses to tensor memory alone, loads or stores: they are complete after
+// tmem_wait_ld or tmem_wait_st, and fence_before_sync before the arrival orders them.
+// Relaxed, since a release first waits for the warp's global loads on their way (900
+// cycles of a K block's 1500 in the large block-scaled product).  What a warp has read
+// from or written to shared memory takes mbar_arrive.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar))
                : "memory");
