@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
         // a cut tile: this warp's part (32 channels) goes to the workspace, and
         // the last of the tile's warps for these channels adds the parts in K
         // order.  The counter's release and acquire cover the warp's stores and
-        // loads (ordered with its lane 0 by the warp's synchronisation).
+        // loads (ordered with its lane 0 by the warp's synchronisation, on either side).
         const int64_t part = int64_t(P::COLS) * 128 * (NT / P::COLS);
         float* dst = partials + (int64_t(blockIdx.x) * 2 + slot) * part + cg * P::COLS * 128 + ch;
         slot = 1;
@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(Split<NT>::THREADS, 1)
                        : "l"(counters + int64_t(tile) * P::EWARPS + (warp - 2))
                        : "memory");
         if (__shfl_sync(0xffffffffu, before, 0) != c1 - c0) continue;
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < P::COLS / 2; ++j) acc[j] = 0;
         for (int c = c0; c <= c1; ++c) {
