@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_relaxed(&sm.pfull[x][buf]);
+        // (a release: the block's scales have been read, and may be written over)
+        if (lane == 0) tc::mbar_arrive(&sm.pfull[x][buf]);
         seen = __all_sync(0xffffffffu, seen);
       }
       if (!ok) break;
