@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][0], sc[nt][1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, mx > m + LAG)) {
+    if (__any_sync(0xffffffffu, moves(mx, m))) {
       const float now = fmaxf(m, mx);
       const float al = now == m ? 1.f : exp2_approx(m - now);
       m = now;

@@ -485,6 +485,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         float sum;
         while (true) {
           const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+          // beyond 2^16 the rounding left over by a fused v mul - m is no longer small against
+          // an exponent (2^95 at 1e36): there scores are rounded first
+          const bool far = fabsf(m) > 65536.f && fabsf(m) <= 3.4028234663852886e38f;
+          const bool special = edge || __any_sync(0xffffffffu, far);
           float mx = -CUDART_INF_F;
           sum = 0.f;
           uint32_t s[2][32];
@@ -494,22 +498,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tmem_wait_ld();
             if (c + 1 < TK / 32) tc::tmem_ld_x32(st + (c + 1) * 32, s[(c + 1) & 1]);
             uint32_t(&v)[32] = s[c & 1];
-            if (edge)
+            if (special) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (tok0 + c * 32 + e >= lim) v[e] = 0xFF800000u;
+              if (far)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float4 f = scl[2 * c + e / 16];
+                  v[e] = __float_as_uint(fmaf(as_f(v[e]), fmaxf(fq * f.x, 1e-37f), f.y));
+                }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 16 positions, of one page
               const float4 f = scl[2 * c + h];
-              const float mul = fmaxf(fq * f.x, 1e-37f);
+              const float mul = far ? 1.f : fmaxf(fq * f.x, 1e-37f), add = far ? 0.f : f.y;
               // (a tree of maxima of three)
               float a[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 a[k] = fmaxf(fmaxf(as_f(v[16 * h + 4 * k]), as_f(v[16 * h + 4 * k + 1])),
                              fmaxf(as_f(v[16 * h + 4 * k + 2]), as_f(v[16 * h + 4 * k + 3])));
-              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), mul, f.y));
-              const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(f.y + off, f.y + off);
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), mul, add));
+              const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(add + off, add + off);
               uint64_t part[2] = {0, 0};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -525,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               sum = fmaf(as_f(uint32_t(part[0])) + as_f(uint32_t(part[0] >> 32)), f.z, sum);
             }
           }
-          if (!__any_sync(0xffffffffu, mx > m + LAG)) break;
+          if (!__any_sync(0xffffffffu, moves(mx, m))) break;
           const float now = fmaxf(m, mx);
           const float al = now == m ? 1.f : exp2_approx(m - now);
           m = now;

@@ -107,6 +107,11 @@ __device__ __forceinline__ void rotated8(const T* row, int d, int pos, const Rop
 constexpr float LAG = 8.f;  // how far a maximum may grow before the sums are rescaled
 constexpr float OFF = 6.f;  // weights are kept 2^OFF above their exponential
 
+// Whether a row's maximum m must move for a score mx: asked of the exponent that mx would
+// get, so that no weight passes 2^(LAG + OFF) whatever m + LAG or OFF - m round to (at 2^27
+// a unit is 16).  False where there is no score.
+__device__ __forceinline__ bool moves(float mx, float m) { return mx + (OFF - m) > LAG + OFF; }
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -156,3 +156,56 @@ def test_a_non_finite_query_stays_in_its_row(mode, value):
         others[i, h] = False
         assert not bool(out[i, h].isfinite().any())
     assert bool(within(st, cache, out, n * G)[others].all())
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_queries_of_zeros_and_of_the_smallest_and_largest_numbers(mode):
+    """Zero queries weigh all positions alike, tiny ones nearly so; scores near the largest
+    number leave a result finite."""
+    dtype, n, G, D = mode
+    st, d, cache = appended(mode, [(n, 100), (1, 1)], I8, 32, seed=11)
+    info = torch.finfo(dtype)
+    st["Q"][0] = 0
+    st["Q"][n - 1, 0] = info.smallest_normal * st["Q"][n - 1, 0].sign()
+    st["Q"][n // 2, 1] = info.max / 1024 * st["Q"][n // 2, 1].sign()
+    Q = st["Q"].contiguous().cuda()
+    out = attend(st, d, Q=Q)
+    others = torch.ones(out.shape[:2], dtype=torch.bool)
+    others[n // 2, 1] = False  # (no bound: its scores are off by more than they differ)
+    assert bool(within(st, cache, out, n * G)[others].all()) and bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("code", [I8, E4])
+@pytest.mark.parametrize("mode", MODES)
+def test_scores_of_every_size(mode, code):
+    """Scores up to 2^110: in the limit a row is the mean value of its largest score.  Queries
+    are 1 and -1, keys whole numbers on scale 1, so that scores are whole multiples of one
+    number: equal ones are equal in the kernel too, others lie 2^10 apart from a scale of 2^10
+    on, where their weights are 0."""
+    dtype, n, G, D = mode
+    L = 200
+    st = plain.make_state([(n, L)], G * 2, 2, D, 16, code, dtype, seed=12)
+    g = torch.Generator().manual_seed(6)
+    st["Q"][:] = torch.where(torch.rand(st["Q"].shape, generator=g) < 0.9, 1.0, -1.0)
+    used = st["table"][0, : -(-L // 16)].long()
+    kq, ks, vq, vs = st["cache"]
+    ks[used] = vs[used] = 1.0
+    base, factor = torch.randint(1, 9, (D,), generator=g), torch.randperm(L, generator=g) % 8
+    for p in range(L):
+        page = int(st["table"][0, p // 16])
+        key = base * (factor[p] if p < L - n else 0)
+        kq[page, :, p % 16] = plain.to_codes(key.float(), code)
+        if p >= L - n:
+            vq[page, :, p % 16] = 0
+    vmax = plain.values(vq[used]).double().nan_to_num(0).abs().amax()
+    d = plain.on_gpu(st)
+    for exponent in (0, 10, 12, 14, 17, 18, 19, 20, 21, 24, 30, 60, 100):
+        scale = 2.0 ** exponent
+        out = attend(st, d, scale=scale)
+        assert bool(out.isfinite().all()), exponent
+        if exponent >= 10:
+            ref, _ = bounds.attention(st["Q"], st["cache"], st["table"], st["cu"], st["lens"],
+                                      None, scale, n * G)
+            # 2^-11 for the f16 weights and as much for exponentials and sums; the result's type
+            err = (out.double() - ref).abs()
+            assert bool((err <= vmax * 2.0 ** -10 + ref.abs() * torch.finfo(dtype).eps / 2).all()), exponent
