@@ -726,7 +726,7 @@ def quantize_fp8_block(A, block_rows=128):
     block_rows 128 for a weight, 1 for activations."""
     R, K = A.shape
     q = A.new_empty((R, K), dtype=torch.uint8)
-    s = A.new_empty((-(-R // block_rows), -(-K // 128)), dtype=torch.float32)
+    s = A.new_empty((-(-R // max(1, block_rows)), -(-K // 128)), dtype=torch.float32)
     wq_quantize_fp8_block(A, block_rows, q, s)
     return q, s
 
