@@ -475,8 +475,11 @@ def wq_gemm_fp8_block(X, Wq, w_scales, Y, ws, stream=None):
     N = Wq.shape[0]
     _holds(X, torch.bfloat16, 0, "X")
     _holds(Y, torch.bfloat16, M * N, "Y")
-    _fits(Wq, N * K, "Wq")
+    if Wq.shape != (N, K) or Wq.element_size() != 1:
+        raise WQError(WQ_ERR_ARG, f"Wq must hold E4M3 codes [N, {K}], got {Wq.dtype} {list(Wq.shape)}")
     _holds(w_scales, torch.float32, -(-N // 128) * -(-K // 128), "w_scales")
+    if w_scales.dim() == 2 and w_scales.shape[1] != -(-K // 128):
+        raise WQError(WQ_ERR_ARG, f"w_scales must have {-(-K // 128)} columns, got {w_scales.shape[1]}")
     _call(_device(X, Wq, w_scales, Y, ws), "wq_gemm_fp8_block", stream, _addr(X), M, K, _addr(Wq),
           _addr(w_scales), N, _addr(Y), _addr(ws), ws.numel() * ws.element_size())
 
