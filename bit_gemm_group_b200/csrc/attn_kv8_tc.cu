@@ -317,6 +317,44 @@ __device__ __forceinline__ void stage_queries(const TQ* __restrict__ Q, const Tc
   }
 }
 
+// Beyond 2^16 what a fused v mul - m leaves over is no longer small against an exponent
+// (2^95 at 1e36): for such a row scores are rounded before the maximum is taken off.
+__device__ __forceinline__ bool is_far(float m) {
+  return fabsf(m) > 65536.f && fabsf(m) <= 3.4028234663852886e38f;
+}
+// The weights of a block (its scores at `st`) against the maximum m, stored over the scores,
+// and their sum, for a warp with such a row; the others as in the kernel's loop.
+// Positions from `lim` on are not seen.  (In the loop: two prompt chunks 336 us back to
+// back where this takes 317.)
+__device__ __noinline__ float far_weights(uint32_t st, const float4* scl, float fq, float m,
+                                          int lim) {
+  const bool far = is_far(m);
+  const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int g = 0; g < TK / 16; ++g) {  // (weights take half the columns of their scores)
+    uint32_t v[16], p[8];
+    tc::tmem_ld_x16(st + g * 16, v);
+    tc::tmem_wait_ld();
+    const float4 f = scl[g];
+    const float mul = fmaxf(fq * f.x, 1e-37f);
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float s = g * 16 + e >= lim ? -CUDART_INF_F : as_f(v[e]);
+      const float x = exp2_approx(far ? fmaf(s, mul, f.y) + off : fmaf(s, mul, f.y + off));
+      part[e & 3] += x;
+      if (e & 1)
+        p[e / 2] = f16x2(as_f(v[e - 1]), x);
+      else
+        v[e] = __float_as_uint(x);
+    }
+    sum = fmaf((part[0] + part[2]) + (part[1] + part[3]), f.z, sum);
+    tc::tmem_st_x8(st + g * 8, p);
+  }
+  return sum;
+}
+
 template <typename TQ, int FMT, int D, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_kv8_tc_kernel(const TQ* __restrict__ Q, TQ* __restrict__ O, Cache c, Batch bt, Rope rp,
@@ -470,6 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m = -CUDART_INF_F, l = 0.f;
       const int t0 = place.t0, J = place.t1 - t0;
       int done = 0;  // of this tile in this segment
+      bool far = false;   // a row of the warp has a maximum beyond 2^16
       bool seen = false;  // the block's scores were complete when the last one's weights were
       for (int j = PAIR ? 0 : x; j < J; j += PAIR ? 1 : 2, ++op, ++done) {
         const uint32_t b = block + uint32_t(j);
@@ -485,10 +524,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         float sum;
         while (true) {
           const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
-          // beyond 2^16 the rounding left over by a fused v mul - m is no longer small against
-          // an exponent (2^95 at 1e36): there scores are rounded first
-          const bool far = fabsf(m) > 65536.f && fabsf(m) <= 3.4028234663852886e38f;
-          const bool special = edge || __any_sync(0xffffffffu, far);
           float mx = -CUDART_INF_F;
           sum = 0.f;
           uint32_t s[2][32];
@@ -498,29 +533,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tmem_wait_ld();
             if (c + 1 < TK / 32) tc::tmem_ld_x32(st + (c + 1) * 32, s[(c + 1) & 1]);
             uint32_t(&v)[32] = s[c & 1];
-            if (special) {
+            if (edge)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (tok0 + c * 32 + e >= lim) v[e] = 0xFF800000u;
-              if (far)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float4 f = scl[2 * c + e / 16];
-                  v[e] = __float_as_uint(fmaf(as_f(v[e]), fmaxf(fq * f.x, 1e-37f), f.y));
-                }
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 16 positions, of one page
               const float4 f = scl[2 * c + h];
-              const float mul = far ? 1.f : fmaxf(fq * f.x, 1e-37f), add = far ? 0.f : f.y;
+              const float mul = fmaxf(fq * f.x, 1e-37f);
               // (a tree of maxima of three)
               float a[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 a[k] = fmaxf(fmaxf(as_f(v[16 * h + 4 * k]), as_f(v[16 * h + 4 * k + 1])),
                              fmaxf(as_f(v[16 * h + 4 * k + 2]), as_f(v[16 * h + 4 * k + 3])));
-              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), mul, add));
-              const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(add + off, add + off);
+              mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), mul, f.y));
+              const uint64_t mul2 = f32x2(mul, mul), add2 = f32x2(f.y + off, f.y + off);
               uint64_t part[2] = {0, 0};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -540,6 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float now = fmaxf(m, mx);
           const float al = now == m ? 1.f : exp2_approx(m - now);
           m = now;
+          far = __any_sync(0xffffffffu, is_far(m));
           l *= al;
           if (done) {
             // the products that add to the result so far are complete
@@ -557,10 +586,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (!ok) break;
+        if (far) sum = far_weights(st, scl, fq, m, lim - tok0);
         l += sum;
         seen = j + (PAIR ? 1 : 2) < J &&
                tc::mbar_test(&sm.sfull[x][(op + 1) & 1u], ((op + 1) >> 1) & 1u);
-        tc::tmem_st_x32(st, p);
+        if (!far) tc::tmem_st_x32(st, p);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -631,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               const int64_t blk = c.block(page, it.h);
               const float ks = __ldg(c.ks + blk), vs = __ldg(c.vs + blk);
               uint4 n4 = make_uint4(0, 0, 0, 0);
-              if (ks != ks || !(vs <= 3.4028234663852886e38f)) {
+              if (!(ks + vs < CUDART_INF_F)) {
                 n4 = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
               } else if (FMT == WQ_W8_E4M3) {
                 n4 = __ldg(reinterpret_cast<const uint4*>(
@@ -779,20 +809,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto convert = [&](uint4 (&w)[N], float& ks, float& vs, int j) {
         const uint32_t s = block % STAGES;
         if (!(ok = tc::wait_warp(&empty[s], ((block / STAGES) & 1u) ^ 1u, wd))) return;
+        const bool hides = (t0 + j + 1) * TK > hidden;  // some row does not see all of it
         if (warp == 8) {
-          // A key scale that is no number or a value scale that is not finite makes the
-          // rows that see it NaN: here, or at the end where some rows do not see it.
-          const bool odd = ks != ks || !(vs <= 3.4028234663852886e38f);
-          const bool skip = vs < 0.f || (odd && (t0 + j + 1) * TK > hidden);
+          // A scale that is no number, or infinite, makes the rows that see it NaN: by its
+          // logarithm here, or at the end where some rows do not see it.
           const float v = fmaxf(vs, 1e-30f);
+          float lv = vs < 0.f ? -CUDART_INF_F : fmaf(ks, 0.f, __log2f(vs < 1e-30f ? 1e-30f : vs));
+          float rv = vs < 0.f ? 0.f : __fdividef(1.f, v);
+          if (hides && !(lv < CUDART_INF_F)) lv = -CUDART_INF_F, rv = 0.f, sm.nans = 1;
           if (lane < TK / 16)
-            sm.scale[block % SCALES][lane] =
-                make_float4(fmaxf(ks, 1e-30f),
-                            skip ? -CUDART_INF_F : odd ? CUDART_NAN_F : __log2f(v),
-                            skip ? 0.f : __fdividef(1.f, v), 0.f);
-          if (odd && skip) sm.nans = 1;
+            sm.scale[block % SCALES][lane] = make_float4(fmaxf(ks, 1e-30f), lv, rv, 0.f);
         }
-        if (FMT == WQ_W8_E4M3 && values && (t0 + j + 1) * TK > hidden) {
+        if (FMT == WQ_W8_E4M3 && values && hides) {
           uint32_t any = 0;
           auto clean = [&](uint32_t& x) {
             const uint32_t b = e4m3_nans(x);
