@@ -8,9 +8,10 @@
 // Bound by HBM up to 8 rows to a kv head: every code is read once per block of 8
 // rows, 2 D bytes per position and head.  64 sequences of 277580 positions in all,
 // 64 heads of 128 over 8 kv heads, one new token each (int8): 119 us with the
-// join, 4.8 TB/s.
+// join on inputs used over and over, 4.8 TB/s; 128 on new ones.
 // Each further block of 8 rows reads the codes again (from L2, mostly) and expands
-// them again: 40 us per 4 x 32768 positions and 8 kv heads.
+// them again: 40 us per 4 x 32768 positions and 8 kv heads.  A block walks over all
+// positions of its sequence, those behind its last row's too (up to the call's rows).
 //
 // The codes go to f16 (exactly: int8 and E4M3 are subsets) and through mma.sync
 // m16n8k16.  The scores' products have 16 rows for 8 queries: rows 0 to 7 hold the

@@ -22,17 +22,19 @@
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
 // Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
-// all (E4M3): 302 us, 779 TFLOP/s of products.  Bound by the hand-offs: a
+// all (E4M3): 318 us on inputs used over and over, 740 TFLOP/s of products; 324 on new
+// ones.  Bound by the hand-offs: a
 // block took a tile 2600 cycles at 431 us, of which its two products are 690
 // (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value
 // step) and its exponentials 512 of the special-function units.  Leaving one
 // part out at a time, at 431 us, says that none of them is the limit by itself: no
 // exponentials 399 us, no converter stores 419, no converter loads either 409, no
 // sums 416; part of the exponentials as polynomials on the fma pipe 430 at best.
-// The steps from there to 302 were the queries, which a row per lane fetched from L2
-// several times over, the weight of an item's start in the division of work, and
-// waits (one that is over already costs 150 cycles): one less per block, the others
-// where nothing waits for them.
+// (Not repeated since.)  The steps from there to 302 were the queries, which a row
+// per lane fetched from L2 several times over, the weight of an item's start in the
+// division of work, and waits (one that is over already costs 150 cycles): one less
+// per block, the others where nothing waits for them.  What a row does not see although
+// it is no number, and scores beyond 2^16, cost the 16 us from 302 to 318.
 // Two score buffers of 64 positions per tile let the tensor cores run while the
 // softmax works on the other.
 //
@@ -1040,14 +1042,14 @@ int launch_tc_by_type(const void* Q, int dtype, int64_t ldq, int64_t heads, cons
 // this, over 4 x 32768 positions of 8 kv heads of 128: 16 rows 117 and 176 us, 24
 // 163 and 176, 32 198 and 176, 40 235 and 176, 64 363 and 178; over 64 x 2048 32
 // rows 206 and 215, 40 247 and 217; heads of 64, 32 rows 135 and 141, 40 165 and
-// 141; over 4 x 1024 40 rows 29 and 33.  Results of
-// 256 elements for two tiles do not fit in tensor memory beside the scores.
+// 141; over 4 x 1024 40 rows 29 and 33.  Heads of 256 are not built here: their results
+// for two tiles do not fit in tensor memory beside the scores (for one they would).
 bool attn_kv8_on_tc(int64_t heads, int64_t kv_heads, int64_t D, int64_t max_q) {
   return D <= 128 && max_q * (heads / kv_heads) > 32;
 }
 // Two row tiles that share the converted blocks: where there are two, and the queries
 // are one term (160 rows over 4 x 32768: 223 us, and 336 one tile after the other; two
-// terms of two tiles do not fit in shared memory beside the blocks).
+// terms of two tiles do not fit in shared memory beside four stages of blocks).
 bool attn_kv8_pairs(int dtype, int64_t heads, int64_t kv_heads, int64_t max_q) {
   return dtype == WQ_BF16 && max_q * (heads / kv_heads) > 128;
 }

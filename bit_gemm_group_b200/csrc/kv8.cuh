@@ -142,8 +142,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // U units in equal runs for up to `most` workers: the first `rem` runs have
-// base + 1 units, the others base.  No run is shorter than two units (a cut run
-// costs a part in the workspace, about a unit's bytes).
+// base + 1 units, the others base.  There are no more runs than make two units each, but
+// for one of an odd U (a cut run costs a part in the workspace, about a unit's bytes).
 struct Runs {
   int64_t base;
   int workers, rem;
