@@ -401,6 +401,11 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
   int seg_tile0 = me.tile;
   // the first unit with positions that not every row of the block sees
   int hides = 0;
+  // the first unit that no row of the block sees any of.  Prompts with heads of 256 walk over
+  // many, and would look for NaN codes in them: 2 x 1024 queries of 8 heads over 2 kv heads
+  // behind 1024 positions 370 us, 423 without the test (int8, which has no such codes, 430,
+  // and 410 without; other calls have 32 rows at most, and so a few such positions)
+  int over = 0;
 
   for (int u = 0; me.at < count; ++u) {
     if (fresh) {
@@ -408,6 +413,10 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
       fresh = false;
       seg_tile0 = me.tile;
       hides = max(0, me.len - me.n + (me.rb * RB) / ar.G + 1) / TK;
+      if (D == 256 && FMT == WQ_W8_E4M3) {
+        const int last = min(me.n - 1, (me.rb * RB + RB - 1) / ar.G);
+        over = (max(0, min(me.len, me.len - me.n + last + 1)) + TK - 1) / TK;
+      }
       // P lanes per row, 32 / P rows at a time; rows are loaded together (all
       // eight, or four of 256 elements) and staged four at a time
       constexpr int P = D / 8, RPP = 32 / P, ITER = RB / RPP, HALF = ITER / 2;
@@ -513,32 +522,35 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
       lv = vs < 0.f ? -CUDART_INF_F : __log2f(vs < 1e-30f ? 1e-30f : vs);  // (NaN stays)
       rv = __fdividef(1.f, v);
     };
+    const bool unseen = D == 256 && FMT == WQ_W8_E4M3 && me.tile >= over;
     float f0, lv0, rv0, f1, lv1, rv1;
-    page_scales(0, f0, lv0, rv0);
-    f1 = f0, lv1 = lv0, rv1 = rv0;
-    if (T_ < TK) page_scales(1, f1, lv1, rv1);
-
-    // -------------------------------------------------- scores
     float sc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      sc[nt][0] = sc[nt][1] = start;
-      sc[nt][2] = sc[nt][3] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
+    if (!unseen) {
+      page_scales(0, f0, lv0, rv0);
+      f1 = f0, lv1 = lv0, rv1 = rv0;
+      if (T_ < TK) page_scales(1, f1, lv1, rv1);
+
+      // -------------------------------------------------- scores
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int r = nt * 8 + g;
-        const uint4 k4 = lds128(st + r * S::KP + swz(D, r, pc) * 16);
-        const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+        sc[nt][0] = sc[nt][1] = start;
+        sc[nt][2] = sc[nt][3] = 0.f;
+      }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t b0, b1;
-          Code<FMT>::key(kw[w], b0, b1);
-          const int ks = j * 4 + w;
-          mma16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
+      for (int j = 0; j < D / 64; ++j) {
+        const int pc = D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = nt * 8 + g;
+          const uint4 k4 = lds128(st + r * S::KP + swz(D, r, pc) * 16);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t b0, b1;
+            Code<FMT>::key(kw[w], b0, b1);
+            const int ks = j * 4 + w;
+            mma16816(sc[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
+          }
         }
       }
     }
@@ -547,85 +559,89 @@ __global__ void __launch_bounds__(Shape<D>::WARPS * 32, 1)
     request_keys();
 
     // -------------------------------------------------- softmax, base 2
-    float mx = -CUDART_INF_F;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const bool hi = NT == 4 && nt >= 2;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        sc[nt][e] = fmaf(sc[nt][e] + sc[nt][2 + e], hi ? f1 : f0, hi ? lv1 : lv0);
-    }
-    if (__any_sync(0xffffffffu, (me.tile + 1) * TK > lim)) {
-      const int left = lim - me.tile * TK - 2 * t;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (nt * 8 + e >= left) sc[nt][e] = -CUDART_INF_F;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][0], sc[nt][1]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, moves(mx, m))) {
-      const float now = fmaxf(m, mx);
-      const float al = now == m ? 1.f : exp2_approx(m - now);
-      m = now;
-      l *= al;
-      const float a0 = __shfl_sync(0xffffffffu, al, t * 8);
-      const float a1 = __shfl_sync(0xffffffffu, al, t * 8 + 4);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        acc[mt][0] *= a0;
-        acc[mt][1] *= a1;
-        acc[mt][2] *= a0;
-        acc[mt][3] *= a1;
-      }
-    }
     uint32_t pb[NT];
-    {
-      const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
-      float s0 = 0.f, s1 = 0.f;
+    if (!unseen) {
+      float mx = -CUDART_INF_F;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float a = exp2_approx(sc[nt][0] + off), b = exp2_approx(sc[nt][1] + off);
-        if (NT == 4 && nt >= 2)
-          s1 += a + b;
-        else
-          s0 += a + b;
-        pb[nt] = f16x2(a, b);
+        const bool hi = NT == 4 && nt >= 2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sc[nt][e] = fmaf(sc[nt][e] + sc[nt][2 + e], hi ? f1 : f0, hi ? lv1 : lv0);
       }
-      l += s0 * rv0 + s1 * rv1;
+      if (__any_sync(0xffffffffu, (me.tile + 1) * TK > lim)) {
+        const int left = lim - me.tile * TK - 2 * t;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (nt * 8 + e >= left) sc[nt][e] = -CUDART_INF_F;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][0], sc[nt][1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      if (__any_sync(0xffffffffu, moves(mx, m))) {
+        const float now = fmaxf(m, mx);
+        const float al = now == m ? 1.f : exp2_approx(m - now);
+        m = now;
+        l *= al;
+        const float a0 = __shfl_sync(0xffffffffu, al, t * 8);
+        const float a1 = __shfl_sync(0xffffffffu, al, t * 8 + 4);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[mt][0] *= a0;
+          acc[mt][1] *= a1;
+          acc[mt][2] *= a0;
+          acc[mt][3] *= a1;
+        }
+      }
+      {
+        const float off = OFF - (m == -CUDART_INF_F ? 0.f : m);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float a = exp2_approx(sc[nt][0] + off), b = exp2_approx(sc[nt][1] + off);
+          if (NT == 4 && nt >= 2)
+            s1 += a + b;
+          else
+            s0 += a + b;
+          pb[nt] = f16x2(a, b);
+        }
+        l += s0 * rv0 + s1 * rv1;
+      }
     }
 
     // -------------------------------------------------- values
     cp_wait<2 * S::STAGES - 1>();
     __syncwarp();
-    if (FMT == WQ_W8_E4M3 && me.tile >= hides) nans |= zero_nans<D>(vb);
+    if (!unseen) {
+      if (FMT == WQ_W8_E4M3 && me.tile >= hides) nans |= zero_nans<D>(vb);
 #pragma unroll
-    for (int ks = 0; ks < TK / 16; ++ks) {
-      const int r = ks * 16 + 2 * t;
-      constexpr int WORDS = D == 64 ? 2 : 4;
+      for (int ks = 0; ks < TK / 16; ++ks) {
+        const int r = ks * 16 + 2 * t;
+        constexpr int WORDS = D == 64 ? 2 : 4;
 #pragma unroll
-      for (int q = 0; q < (D == 64 ? 1 : D / 128); ++q) {
-        uint32_t w[4][4];
+        for (int q = 0; q < (D == 64 ? 1 : D / 128); ++q) {
+          uint32_t w[4][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // positions r, r + 1, r + 8, r + 9
-          const int row = r + (k & 1) + 8 * (k >> 1);
-          if (D == 64) {
-            const uint2 x = lds64(vb + row * S::VP + g * 8);
-            w[k][0] = x.x, w[k][1] = x.y;
-          } else {
-            const uint4 x = lds128(vb + row * S::VP + swz(D, row, g + 8 * q) * 16);
-            w[k][0] = x.x, w[k][1] = x.y, w[k][2] = x.z, w[k][3] = x.w;
+          for (int k = 0; k < 4; ++k) {  // positions r, r + 1, r + 8, r + 9
+            const int row = r + (k & 1) + 8 * (k >> 1);
+            if (D == 64) {
+              const uint2 x = lds64(vb + row * S::VP + g * 8);
+              w[k][0] = x.x, w[k][1] = x.y;
+            } else {
+              const uint4 x = lds128(vb + row * S::VP + swz(D, row, g + 8 * q) * 16);
+              w[k][0] = x.x, w[k][1] = x.y, w[k][2] = x.z, w[k][3] = x.w;
+            }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 2 * WORDS; ++k) {
-          uint32_t a0, a1, a2, a3;
-          Code<FMT>::value(w[0][k >> 1], w[1][k >> 1], k & 1, a0, a1);
-          Code<FMT>::value(w[2][k >> 1], w[3][k >> 1], k & 1, a2, a3);
-          mma16816(acc[q * 8 + k], a0, a1, a2, a3, pb[2 * ks], pb[2 * ks + 1]);
+          for (int k = 0; k < 2 * WORDS; ++k) {
+            uint32_t a0, a1, a2, a3;
+            Code<FMT>::value(w[0][k >> 1], w[1][k >> 1], k & 1, a0, a1);
+            Code<FMT>::value(w[2][k >> 1], w[3][k >> 1], k & 1, a2, a3);
+            mma16816(acc[q * 8 + k], a0, a1, a2, a3, pb[2 * ks], pb[2 * ks + 1]);
+          }
         }
       }
     }

@@ -22,7 +22,7 @@
 // terms (rounded, and what that left) so that a result is good to fp16.
 //
 // Two chunks, 3245 queries of 32 heads over 8 kv heads of 128, 9974 positions in
-// all (E4M3): 318 us on inputs used over and over, 740 TFLOP/s of products; 324 on new
+// all (E4M3): 314 us on inputs used over and over, 750 TFLOP/s of products; 322 on new
 // ones.  Bound by the hand-offs: a
 // block took a tile 2600 cycles at 431 us, of which its two products are 690
 // (45 to 52 cycles per m128 n64 k16 score step, 60 to 68 per m128 n128 k16 value
@@ -34,7 +34,7 @@
 // per lane fetched from L2 several times over, the weight of an item's start in the
 // division of work, and waits (one that is over already costs 150 cycles): one less
 // per block, the others where nothing waits for them.  What a row does not see although
-// it is no number, and scores beyond 2^16, cost the 16 us from 302 to 318.
+// it is no number, and scores beyond 2^16, cost the 12 us from 302 to 314.
 // Two score buffers of 64 positions per tile let the tensor cores run while the
 // softmax works on the other.
 //
@@ -71,6 +71,7 @@ constexpr int START = 11;
 struct Item {
   int b, r, h;
   int n, q0, len, R, tiles;
+  int hidden;  // first position that some query of the row tile does not see
   __device__ __forceinline__ void load(const Batch& bt, int tshift, int G, int rows, int* status) {
     n = seq_rows(bt, b, &q0, status);
     len = __ldg(bt.lens + b);
@@ -88,13 +89,10 @@ struct Item {
     int seen = len - n + int(i) + 1;
     seen = seen > len ? len : seen;
     tiles = seen > 0 ? (seen + TK - 1) / TK : 1;
+    hidden = len - n + int(int64_t(r) * rows / G) + 1;
+    hidden = hidden < 0 ? 0 : hidden < len ? hidden : len;
   }
   __device__ __forceinline__ bool valid() const { return n > 0 && r < R; }
-  // the first position that not every query of the row tile sees
-  __device__ __forceinline__ int first_hidden(int G, int rows) const {
-    const int seen = len - n + int(int64_t(r) * rows / G) + 1;
-    return seen < 0 ? 0 : seen < len ? seen : len;
-  }
 };
 
 // Walks over the work of a CTA's run: the item and its blocks [t0, t1).
@@ -319,6 +317,14 @@ __device__ __forceinline__ void stage_queries(const TQ* __restrict__ Q, const Tc
   }
 }
 
+template <typename T>
+__device__ __forceinline__ T nan_of() {
+  if constexpr (std::is_same<T, __half>::value)
+    return __float2half_rn(CUDART_NAN_F);
+  else
+    return __float2bfloat16_rn(CUDART_NAN_F);
+}
+
 // Beyond 2^16 what a fused v mul - m leaves over is no longer small against an exponent
 // (2^95 at 1e36): for such a row scores are rounded before the maximum is taken off.
 __device__ __forceinline__ bool is_far(float m) {
@@ -327,7 +333,7 @@ __device__ __forceinline__ bool is_far(float m) {
 // The weights of a block (its scores at `st`) against the maximum m, stored over the scores,
 // and their sum, for a warp with such a row; the others as in the kernel's loop.
 // Positions from `lim` on are not seen.  (In the loop: two prompt chunks 336 us back to
-// back where this takes 317.)
+// back where this takes 313.)
 __device__ __noinline__ float far_weights(uint32_t st, const float4* scl, float fq, float m,
                                           int lim) {
   const bool far = is_far(m);
@@ -588,11 +594,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (!ok) break;
-        if (far) sum = far_weights(st, scl, fq, m, lim - tok0);
-        l += sum;
         seen = j + (PAIR ? 1 : 2) < J &&
                tc::mbar_test(&sm.sfull[x][(op + 1) & 1u], ((op + 1) >> 1) & 1u);
-        if (!far) tc::tmem_st_x32(st, p);
+        if (far)
+          sum = far_weights(st, scl, fq, m, lim - tok0);
+        else
+          tc::tmem_st_x32(st, p);
+        l += sum;
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -637,7 +645,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + it.h * ar.G + (rr - i * ar.G)) * D;
         float* pd = ar.parts + (part * ROWS + prow) * D;
-        const bool nans = live && sm.nans != 0;
         if (!whole) {
           __stcg(ar.part_ml + (part * ROWS + prow) * 2, m);
           __stcg(ar.part_ml + (part * ROWS + prow) * 2 + 1, l);
@@ -653,29 +660,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 16; ++e) {
             v[e] = __uint_as_float(a[e]) * w0;
             if (both) v[e] = fmaf(__uint_as_float(b[e]), w1, v[e]);
-          }
-          if (nans) {
-            const int end = min(lim, place.t1 * TK);
-#pragma unroll 1
-            for (int p = max(t0, it.first_hidden(ar.G, ROWS) / TK) * TK; p < end; ++p) {
-              const int page = __ldg(bt.table + int64_t(it.b) * bt.width + (p >> c.tshift));
-              if (page < 0 || page >= c.pages) continue;
-              const int64_t blk = c.block(page, it.h);
-              const float ks = __ldg(c.ks + blk), vs = __ldg(c.vs + blk);
-              uint4 n4 = make_uint4(0, 0, 0, 0);
-              if (!(ks + vs < CUDART_INF_F)) {
-                n4 = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-              } else if (FMT == WQ_W8_E4M3) {
-                n4 = __ldg(reinterpret_cast<const uint4*>(
-                    c.vq + ((blk << c.tshift) + (p & (T_ - 1))) * D + q * 16));
-                n4 = make_uint4(e4m3_nans(n4.x), e4m3_nans(n4.y), e4m3_nans(n4.z), e4m3_nans(n4.w));
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t w = e < 4 ? n4.x : e < 8 ? n4.y : e < 12 ? n4.z : n4.w;
-                if (w >> (8 * (e & 3)) & 0x80u) v[e] = CUDART_NAN_F;
-              }
-            }
           }
           if (!whole) {
 #pragma unroll
@@ -697,6 +681,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                   y.e[e] = __float2bfloat16_rn(v[e0 + e] * inv);
               }
               *reinterpret_cast<uint4*>(dst + q * 16 + e0) = y.u;
+            }
+          }
+        }
+      }
+      if (sm.nans != 0 && live && (PAIR || x == 0)) {
+        // what the row does see of what its blocks left out, over the results
+        const bool to_part = !whole;
+        const int64_t prow = part * ROWS + (PAIR ? x * 128 : 0) + row;
+        TQ* dst = O + (int64_t(it.q0 + i) * ar.heads + it.h * ar.G + (rr - i * ar.G)) * D;
+        const int end = min(lim, place.t1 * TK);
+#pragma unroll 1
+        for (int p = max(t0, it.hidden / TK) * TK; p < end; ++p) {
+          const int page = __ldg(bt.table + int64_t(it.b) * bt.width + (p >> c.tshift));
+          if (page < 0 || page >= c.pages) continue;
+          const int64_t blk = c.block(page, it.h);
+          const bool all = !(__ldg(c.ks + blk) + __ldg(c.vs + blk) < CUDART_INF_F);
+          const uint8_t* v = c.vq + ((blk << c.tshift) + (p & (T_ - 1))) * D;
+          if (FMT != WQ_W8_E4M3 && !all) continue;
+#pragma unroll 1
+          for (int e0 = 0; e0 < D; e0 += 4) {
+            const uint32_t b =
+                all ? 0x80808080u : e4m3_nans(__ldg(reinterpret_cast<const uint32_t*>(v + e0)));
+            if (b == 0) continue;
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              if (!(b >> (8 * e) & 0x80u)) continue;
+              if (to_part)
+                __stcg(ar.parts + prow * D + e0 + e, CUDART_NAN_F);
+              else
+                dst[e0 + e] = nan_of<TQ>();
             }
           }
         }
@@ -733,7 +747,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (; more && ok; more = step()) {
       const int t0 = place.t0, J = place.t1 - t0, len = it.len;
-      const int hidden = it.first_hidden(ar.G, ROWS);
       // Lane g of a warp looks after positions 16 g to 16 g + 15 of a block (one
       // page): table entry two blocks ahead, address and (first warp) scales one
       // block ahead, so that nothing here waits for the load before it.
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto convert = [&](uint4 (&w)[N], float& ks, float& vs, int j) {
         const uint32_t s = block % STAGES;
         if (!(ok = tc::wait_warp(&empty[s], ((block / STAGES) & 1u) ^ 1u, wd))) return;
-        const bool hides = (t0 + j + 1) * TK > hidden;  // some row does not see all of it
+        const bool hides = (t0 + j + 1) * TK > it.hidden;  // some row does not see all of it
         if (warp == 8) {
           // A scale that is no number, or infinite, makes the rows that see it NaN: by its
           // logarithm here, or at the end where some rows do not see it.
